@@ -6,4 +6,4 @@ the thin ctypes binding (ecasq.py) and the seeded input generators
 (workloads.py). There is no CPU fallback: the first call into the binding
 raises if the CUDA library is missing.
 """
-__all__ = ["ecasq", "workloads"]
+__all__ = ["ecasq", "linear", "workloads"]

@@ -77,6 +77,22 @@ size_t approx_ws(void* ws, int n, int p, const ApproxPlan& plan, SolveWs* w) {
   return c.off;
 }
 
+// 8-bit operators: element type, sizes and the layout of an 8-bit matrix.
+constexpr int64_t kMaxRows8 = INT32_MAX;
+constexpr int64_t kMaxCols8 = int64_t(1) << 27;
+constexpr int64_t kMaxK8 = 131072;  // 127^2 * 131072 < 2^31
+
+bool valid_type(int type) { return type == ECASQ_F32 || type == ECASQ_BF16 || type == ECASQ_F16; }
+bool valid_rows(int64_t n, int64_t k) { return n >= 0 && n <= kMaxRows8 && k >= 1 && k <= kMaxCols8; }
+// A matrix of n rows with pitch ld: the pitch of a single row says nothing.
+bool valid_pitch(int64_t n, int64_t k, int64_t ld) { return n <= 1 || ld >= k; }
+bool valid_bytes(const void* p, int64_t k, int64_t ld, int64_t to) {
+  return p && (reinterpret_cast<uintptr_t>(p) & 15) == 0 && ld >= k && ld % to == 0;
+}
+bool valid_checkpoint(const void* q, int64_t ldq, const void* scale, int64_t lds, int64_t k) {
+  return valid_bytes(q, k, ldq, 32) && valid_bytes(scale, (k + 31) / 32, lds, 16);
+}
+
 }  // namespace
 
 void note_launch() { ++g_launches; }
@@ -480,5 +496,63 @@ int ecasq_entropy(const int64_t* hist, int n, int s, double* H, void* stream) {
   if (!hist || !H || n < 1 || s < 1 || s > 256) return ECASQ_ERR_ARG;
   return cuda_status(launch_entropy(hist, n, s, H, static_cast<cudaStream_t>(stream)));
 }
+
+int ecasq_int8_quantize(const void* X, int x_type, int64_t n, int64_t k, int64_t ldx, int8_t* q, int64_t ldq,
+                        float* scale, int32_t* status, void* stream) {
+  if (!valid_type(x_type) || !valid_rows(n, k)) return ECASQ_ERR_ARG;
+  if (n == 0) return ECASQ_OK;
+  if (!X || !valid_pitch(n, k, ldx) || !valid_bytes(q, k, ldq, 16) || !scale || !status) return ECASQ_ERR_ARG;
+  return cuda_status(
+      launch_int8_quantize(X, x_type, n, k, ldx, q, ldq, scale, status, static_cast<cudaStream_t>(stream)));
+}
+
+int ecasq_int8_matmul(const int8_t* A, int64_t lda, const float* sa, const int8_t* B, int64_t ldb, const float* sb,
+                      const float* bias, int64_t m, int64_t n, int64_t k, void* Y, int y_type, int64_t ldy,
+                      void* stream) {
+  if (!valid_type(y_type) || !valid_rows(m, k) || n < 1 || n > kMaxRows8 || k > kMaxK8) return ECASQ_ERR_ARG;
+  if (m == 0) return ECASQ_OK;
+  if (!valid_bytes(A, k, lda, 16) || !valid_bytes(B, k, ldb, 16) || !sa || !sb || !Y || !valid_pitch(m, n, ldy))
+    return ECASQ_ERR_ARG;
+  return cuda_status(launch_int8_matmul(A, lda, sa, B, ldb, sb, bias, m, n, k, Y, y_type, ldy,
+                                        static_cast<cudaStream_t>(stream)));
+}
+
+int ecasq_checkpoint8(const void* X, int x_type, int64_t t, int64_t k, int64_t ldx, uint64_t seed,
+                      const uint64_t* seed_add, int8_t* q, int64_t ldq, uint8_t* scale, int64_t lds, void* stream) {
+  if (!valid_type(x_type) || !valid_rows(t, k)) return ECASQ_ERR_ARG;
+  if (t == 0) return ECASQ_OK;
+  if (!X || !valid_pitch(t, k, ldx) || !valid_checkpoint(q, ldq, scale, lds, k)) return ECASQ_ERR_ARG;
+  return cuda_status(launch_checkpoint8(X, x_type, t, k, ldx, seed, seed_add, q, ldq, scale, lds,
+                                        static_cast<cudaStream_t>(stream)));
+}
+
+int ecasq_checkpoint8_restore(const int8_t* q, int64_t ldq, const uint8_t* scale, int64_t lds, int64_t t, int64_t k,
+                              void* X, int x_type, int64_t ldx, void* stream) {
+  if (!valid_type(x_type) || !valid_rows(t, k)) return ECASQ_ERR_ARG;
+  if (t == 0) return ECASQ_OK;
+  if (!X || !valid_pitch(t, k, ldx) || !valid_checkpoint(q, ldq, scale, lds, k)) return ECASQ_ERR_ARG;
+  return cuda_status(
+      launch_checkpoint8_restore(q, ldq, scale, lds, t, k, X, x_type, ldx, static_cast<cudaStream_t>(stream)));
+}
+
+size_t ecasq_checkpoint8_wgrad_workspace_size(int64_t t, int64_t o, int64_t k, int dy_type, int64_t ldy) {
+  if (!valid_type(dy_type) || !valid_rows(t, k) || o < 1 || o > kMaxCols8) return 0;
+  return checkpoint8_wgrad_workspace(t, o, k, dy_type, ldy);
+}
+
+int ecasq_checkpoint8_wgrad(const void* dY, int dy_type, int64_t ldy, const int8_t* q, int64_t ldq,
+                            const uint8_t* scale, int64_t lds, int64_t t, int64_t o, int64_t k, void* dW, int dw_type,
+                            int64_t ldw, void* ws, size_t ws_bytes, void* stream) {
+  if (!valid_type(dy_type) || !valid_type(dw_type) || !valid_rows(t, k) || o < 1 || o > kMaxCols8)
+    return ECASQ_ERR_ARG;
+  if (!dW || !valid_pitch(o, k, ldw)) return ECASQ_ERR_ARG;
+  if (t > 0 && (!dY || !valid_pitch(t, o, ldy) || !valid_checkpoint(q, ldq, scale, lds, k))) return ECASQ_ERR_ARG;
+  const size_t need = checkpoint8_wgrad_workspace(t, o, k, dy_type, ldy);
+  if (need && (!ws || ws_bytes < need)) return ECASQ_ERR_WORKSPACE;
+  return cuda_status(launch_checkpoint8_wgrad(dY, dy_type, ldy, q, ldq, scale, lds, t, o, k, dW, dw_type, ldw, ws,
+                                              static_cast<cudaStream_t>(stream)));
+}
+
+int ecasq_device_stalled(void) { return ECASQ_OK; }
 
 }  // extern "C"

@@ -184,4 +184,22 @@ cudaError_t launch_dequantize(const uint8_t* idx, const double* P, int n, int64_
                               const int32_t* Q1, const int32_t* Q1_len, const int32_t* Q2, const int32_t* Q2_len,
                               const double* theta, uint64_t seed, float* Xhat, int32_t* status, cudaStream_t st);
 
+// ---- linear layer in 8-bit integers (int8.cu) ----
+cudaError_t launch_int8_quantize(const void* X, int type, int64_t n, int64_t k, int64_t ldx, int8_t* q, int64_t ldq,
+                                 float* scale, int32_t* status, cudaStream_t st);
+cudaError_t launch_int8_matmul(const int8_t* A, int64_t lda, const float* sa, const int8_t* B, int64_t ldb,
+                               const float* sb, const float* bias, int64_t m, int64_t n, int64_t k, void* Y, int type,
+                               int64_t ldy, cudaStream_t st);
+
+// ---- activation checkpoints in 8 bits (checkpoint8.cu) ----
+cudaError_t launch_checkpoint8(const void* X, int type, int64_t t, int64_t k, int64_t ldx, uint64_t seed,
+                               const uint64_t* seed_add, int8_t* q, int64_t ldq, uint8_t* scale, int64_t lds,
+                               cudaStream_t st);
+cudaError_t launch_checkpoint8_restore(const int8_t* q, int64_t ldq, const uint8_t* scale, int64_t lds, int64_t t,
+                                       int64_t k, void* X, int type, int64_t ldx, cudaStream_t st);
+size_t checkpoint8_wgrad_workspace(int64_t t, int64_t o, int64_t k, int dy_type, int64_t ldy);
+cudaError_t launch_checkpoint8_wgrad(const void* dY, int dy_type, int64_t ldy, const int8_t* q, int64_t ldq,
+                                     const uint8_t* scale, int64_t lds, int64_t t, int64_t o, int64_t k, void* dW,
+                                     int dw_type, int64_t ldw, void* ws, cudaStream_t st);
+
 }  // namespace ecasq

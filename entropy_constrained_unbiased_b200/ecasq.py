@@ -24,6 +24,8 @@ EXPORTS = [
     "ecasq_solve_approx_budget_stats",
     "ecasq_encode", "ecasq_dequantize", "ecasq_entropy", "ecasq_rans_segments", "ecasq_rans_segment_words",
     "ecasq_rans_encode", "ecasq_rans_decode", "ecasq_status_string", "ecasq_launch_count",
+    "ecasq_int8_quantize", "ecasq_int8_matmul", "ecasq_checkpoint8", "ecasq_checkpoint8_restore",
+    "ecasq_checkpoint8_wgrad_workspace_size", "ecasq_checkpoint8_wgrad", "ecasq_device_stalled",
 ]
 
 
@@ -75,6 +77,13 @@ def load(path: str = LIB_PATH):
         "ecasq_rans_decode": (I, [P, P, P, P, I, I, I64, I, U64, P, P, P]),
         "ecasq_status_string": (C.c_char_p, [I]),
         "ecasq_launch_count": (C.c_uint64, [I]),
+        "ecasq_int8_quantize": (I, [P, I, I64, I64, I64, P, I64, P, P, P]),
+        "ecasq_int8_matmul": (I, [P, I64, P, P, I64, P, P, I64, I64, I64, P, I, I64, P]),
+        "ecasq_checkpoint8": (I, [P, I, I64, I64, I64, U64, P, P, I64, P, I64, P]),
+        "ecasq_checkpoint8_restore": (I, [P, I64, P, I64, I64, I64, P, I, I64, P]),
+        "ecasq_checkpoint8_wgrad_workspace_size": (SZ, [I64, I64, I64, I, I64]),
+        "ecasq_checkpoint8_wgrad": (I, [P, I, I64, P, I64, P, I64, I64, I64, I64, P, I, I64, P, SZ, P]),
+        "ecasq_device_stalled": (I, []),
     }
     for name, (res, args) in sig.items():
         fn = getattr(L, name)
@@ -456,3 +465,167 @@ def rans_decode(words: torch.Tensor, seg_len: torch.Tensor, hist: torch.Tensor, 
                                int(bool(two_codes)), n, d, s, C.c_uint64(seed), _ptr(idx), _ptr(st), _stream()),
            "ecasq_rans_decode")
     return idx, st
+
+
+# -- 8-bit operators: integer linear layer, activation checkpoints ----------------------
+
+_TYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
+
+
+def _matrix(t, name, dtypes, device=None):
+    """Checks a [rows, cols] CUDA matrix with adjacent columns; returns (rows, cols, row pitch)."""
+    if not t.is_cuda or t.dtype not in dtypes or t.dim() != 2:
+        raise EcasqError(f"{name} must be a 2-D CUDA tensor of {' or '.join(str(d) for d in dtypes)}")
+    if device is not None and t.device != device:
+        raise EcasqError(f"{name} is on {t.device}, not {device}")
+    n, k = t.shape
+    if k < 1 or (k > 1 and t.stride(1) != 1):
+        raise EcasqError(f"{name} must have at least one column and adjacent columns")
+    ld = t.stride(0) if n > 1 else k
+    if ld < k:
+        raise EcasqError(f"{name} has overlapping rows (stride {ld} for {k} columns)")
+    return n, k, ld
+
+
+def _matrix8(t, name, dtype, to, device=None):
+    """Checks a matrix of 8-bit values whose rows lie in a whole number of `to` bytes."""
+    n, k, ld = _matrix(t, name, (dtype,), device)
+    if n <= 1:
+        ld = (k + to - 1) // to * to
+        whole = t.untyped_storage().nbytes() - t.storage_offset() >= n * ld
+    else:
+        whole = ld % to == 0
+    if not whole or t.data_ptr() % 16 != 0:
+        raise EcasqError(f"{name} must lie in 16-byte aligned rows of a whole number of {to} bytes, as this module's "
+                         "own calls return it")
+    return n, k, ld
+
+
+def _vector(t, name, dtype, n, device):
+    if t.dtype != dtype or t.dim() != 1 or t.shape[0] != n or t.device != device or (n > 1 and t.stride(0) != 1):
+        raise EcasqError(f"{name} must be a contiguous {dtype} tensor of {n} entries on {device}")
+    return t.data_ptr()
+
+
+def _rows8(n, k, to, dtype, device):
+    """Uninitialised 8-bit values [n, k] in rows of a whole number of `to` bytes."""
+    return torch.empty((n, (k + to - 1) // to * to), dtype=dtype, device=device)
+
+
+def _call(name, device, *args):
+    """One call of the library on the current stream of `device`."""
+    fn = getattr(_lib, name)
+    if device.index == torch.cuda.current_device():
+        rc = fn(*args, torch.cuda.current_stream().cuda_stream)
+    else:
+        with torch.cuda.device(device):
+            rc = fn(*args, torch.cuda.current_stream().cuda_stream)
+    _check(rc, name)
+
+
+def int8_quantize(X: torch.Tensor):
+    """Rows of X (float32, bfloat16 or float16 [n, k]) in 8-bit integers with one
+    scale per row: q int8 [n, k], scale float32 [n], status int32 [n], with
+    X ~ q * scale[:, None] and q the nearest integers to 127 X / max |row|."""
+    _need_cuda()
+    n, k, ld = _matrix(X, "X", _TYPES)
+    dev = X.device
+    q = _rows8(n, k, 32, torch.int8, dev)
+    scale = torch.empty(n, dtype=torch.float32, device=dev)
+    st = torch.empty(n, dtype=torch.int32, device=dev)
+    _call("ecasq_int8_quantize", dev, X.data_ptr(), _TYPES[X.dtype], n, k, ld, q.data_ptr(), q.shape[1],
+          scale.data_ptr(), st.data_ptr())
+    return q[:, :k], scale, st
+
+
+def int8_matmul(A: torch.Tensor, sa: torch.Tensor, B: torch.Tensor, sb: torch.Tensor, bias=None,
+                out_dtype=torch.bfloat16):
+    """Y [m, n] = (A B^T) * sa[:, None] * sb + bias from int8 A [m, k] (tokens) and
+    B [n, k] (output channels) as int8_quantize returns them; bias float32 [n]."""
+    _need_cuda()
+    dev = A.device
+    m, k, lda = _matrix8(A, "A", torch.int8, 16)
+    n, kb, ldb = _matrix8(B, "B", torch.int8, 16, dev)
+    if kb != k:
+        raise EcasqError(f"A has {k} columns and B {kb}")
+    if k > 131072:
+        raise EcasqError(f"sums of {k} products do not fit in 32 bits (at most 131072)")
+    if n < 1:
+        raise EcasqError("B must have at least one row")
+    if out_dtype not in _TYPES:
+        raise EcasqError(f"out_dtype must be float32, bfloat16 or float16, not {out_dtype}")
+    Y = torch.empty((m, n), dtype=out_dtype, device=dev)
+    _call("ecasq_int8_matmul", dev, A.data_ptr(), lda, _vector(sa, "sa", torch.float32, m, dev), B.data_ptr(), ldb,
+          _vector(sb, "sb", torch.float32, n, dev),
+          None if bias is None else _vector(bias, "bias", torch.float32, n, dev), m, n, k, Y.data_ptr(),
+          _TYPES[out_dtype], n)
+    return Y
+
+
+def checkpoint8(X: torch.Tensor, seed):
+    """X (float32, bfloat16 or float16 [t, k]) in 8 bits, rounded without bias:
+    q int8 [t, k] and the scale bytes uint8 [t, ceil(k / 32)] of its blocks of 32
+    entries. `seed` is an integer, or a CUDA int64 tensor of one entry read when
+    the call runs (a graph's replays then draw new bits when it changes)."""
+    _need_cuda()
+    t, k, ld = _matrix(X, "X", _TYPES)
+    dev = X.device
+    word = None
+    if isinstance(seed, torch.Tensor):
+        if seed.dtype != torch.int64 or seed.numel() != 1 or seed.device != dev:
+            raise EcasqError(f"a seed tensor must hold one int64 on {dev}")
+        seed, word = 0, seed.data_ptr()
+    blocks = (k + 31) // 32
+    q = _rows8(t, k, 32, torch.int8, dev)
+    s = _rows8(t, blocks, 16, torch.uint8, dev)
+    _call("ecasq_checkpoint8", dev, X.data_ptr(), _TYPES[X.dtype], t, k, ld, seed & 0xFFFFFFFFFFFFFFFF, word,
+          q.data_ptr(), q.shape[1], s.data_ptr(), s.shape[1])
+    return q[:, :k], s[:, :blocks]
+
+
+def _checkpoint(q, scale):
+    t, k, ldq = _matrix8(q, "q", torch.int8, 32)
+    ts, blocks, lds = _matrix8(scale, "scale", torch.uint8, 16, q.device)
+    if ts != t or blocks != (k + 31) // 32:
+        raise EcasqError(f"scale must be [{t}, {(k + 31) // 32}] for q [{t}, {k}], not {list(scale.shape)}")
+    return t, k, ldq, lds
+
+
+def checkpoint8_restore(q: torch.Tensor, scale: torch.Tensor, dtype=torch.float32):
+    """The values of a checkpoint as a [t, k] tensor of dtype."""
+    _need_cuda()
+    t, k, ldq, lds = _checkpoint(q, scale)
+    if dtype not in _TYPES:
+        raise EcasqError(f"dtype must be float32, bfloat16 or float16, not {dtype}")
+    X = torch.empty((t, k), dtype=dtype, device=q.device)
+    _call("ecasq_checkpoint8_restore", q.device, q.data_ptr(), ldq, scale.data_ptr(), lds, t, k, X.data_ptr(),
+          _TYPES[dtype], k)
+    return X
+
+
+def checkpoint8_wgrad(dY: torch.Tensor, q: torch.Tensor, scale: torch.Tensor, out_dtype=None):
+    """dW [o, k] = dY^T X^ from dY [t, o] and the checkpoint (q, scale) of X [t, k];
+    out_dtype is dY's unless given."""
+    L = _need_cuda()
+    dev = dY.device
+    t, o, ldy = _matrix(dY, "dY", _TYPES)
+    tq, k, ldq, lds = _checkpoint(q, scale)
+    if tq != t or q.device != dev:
+        raise EcasqError(f"dY has {t} rows on {dev}, the checkpoint {tq} on {q.device}")
+    out_dtype = dY.dtype if out_dtype is None else out_dtype
+    if out_dtype not in _TYPES:
+        raise EcasqError(f"out_dtype must be float32, bfloat16 or float16, not {out_dtype}")
+    dW = torch.empty((o, k), dtype=out_dtype, device=dev)
+    ty = _TYPES[dY.dtype]
+    need = L.ecasq_checkpoint8_wgrad_workspace_size(t, o, k, ty, ldy)
+    # the caching allocator's, so that it belongs to this call (or to the graph that captures it) alone
+    ws = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
+    _call("ecasq_checkpoint8_wgrad", dev, dY.data_ptr(), ty, ldy, q.data_ptr(), ldq, scale.data_ptr(), lds, t, o, k,
+          dW.data_ptr(), _TYPES[out_dtype], k, ws.data_ptr() if need else None, need)
+    return dW
+
+
+def check_stalled():
+    """Waits for the current device and raises if a tensor-core kernel of this
+    library gave up on one of its copies since the last check."""
+    _check(_need_cuda().ecasq_device_stalled(), "a bounded device wait gave up")

@@ -1,0 +1,76 @@
+"""Linear layers on 8-bit data: the integer product for serving, and training
+with 8-bit activation checkpoints.
+
+`int8_linear` quantises its tokens and multiplies them by 8-bit weights.
+`checkpoint_linear` is F.linear for training: the forward product is the plain
+one, but what it keeps of its input for the backward pass is the unbiased 8-bit
+checkpoint, about half the bytes of bfloat16. The weight gradient is linear in
+the input, so its mean over the rounding is the exact gradient; the input's and
+the bias's gradients do not use the checkpoint.
+
+The operators are the library's kernels (ecasq.py); there is no CPU path.
+"""
+from __future__ import annotations
+
+import torch
+import torch.nn.functional as F
+
+from . import ecasq as E
+
+
+def int8_linear(x: torch.Tensor, weight: torch.Tensor, weight_scale: torch.Tensor, bias=None) -> torch.Tensor:
+    """x [..., k] (float32, bfloat16 or float16) times 8-bit weights: quantises each
+    token and multiplies, Y [..., n] in x's type. weight int8 [n, k] and
+    weight_scale float32 [n] are ecasq.int8_quantize's of the layer's weight
+    matrix; bias float32 [n]. For serving: it has no gradient, and refuses an x
+    that asks for one."""
+    if torch.is_grad_enabled() and x.requires_grad:
+        raise E.EcasqError("int8_linear has no gradient; use checkpoint_linear for training, or torch.no_grad()")
+    rows = x if x.dim() == 2 else x.reshape(-1, x.shape[-1])
+    q, scale, _ = E.int8_quantize(rows)
+    y = E.int8_matmul(q, scale, weight, weight_scale, bias, x.dtype)
+    return y if x.dim() == 2 else y.reshape(*x.shape[:-1], y.shape[1])
+
+
+class _CheckpointLinear(torch.autograd.Function):
+    @staticmethod
+    @torch.amp.custom_fwd(device_type="cuda")
+    def forward(ctx, x, weight, bias, seed):
+        ctx.rows = x.shape[:-1]
+        if ctx.needs_input_grad[1]:
+            q, scale = E.checkpoint8(x.reshape(-1, x.shape[-1]), seed)
+        else:
+            q = scale = None
+        ctx.save_for_backward(q, scale, weight if ctx.needs_input_grad[0] else None)
+        ctx.dtypes = x.dtype, weight.dtype, None if bias is None else bias.dtype
+        return F.linear(x, weight, bias)
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    @torch.amp.custom_bwd(device_type="cuda")
+    def backward(ctx, dy):
+        q, scale, weight = ctx.saved_tensors
+        x_type, w_type, b_type = ctx.dtypes
+        dx = dw = db = None
+        if ctx.needs_input_grad[0]:
+            dx = torch.matmul(dy, weight).to(x_type)
+        rows = dy.reshape(-1, dy.shape[-1])
+        if ctx.needs_input_grad[1]:
+            if rows.stride(1) != 1 or (rows.shape[0] > 1 and rows.stride(0) < rows.shape[1]):
+                rows = rows.contiguous()  # an expanded gradient, such as that of a sum
+            dw = E.checkpoint8_wgrad(rows, q, scale, w_type)
+        if ctx.needs_input_grad[2]:
+            db = rows.sum(0, dtype=torch.float32).to(b_type)
+        return dx, dw, db, None
+
+
+def checkpoint_linear(x: torch.Tensor, weight: torch.Tensor, bias=None, *, seed) -> torch.Tensor:
+    """x [..., k] W^T + bias, keeping x for the backward pass in 8 bits (unbiased,
+    keyed by `seed`: another value for each layer and step, so that roundings are
+    independent; an integer, or a CUDA int64 tensor of one entry for graphs).
+    weight [n, k] and bias [n] in x's type, or in any under autocast."""
+    if x.device.type != "cuda" or weight.device != x.device:
+        raise E.EcasqError("checkpoint_linear needs x and weight on one CUDA device; there is no CPU path")
+    if weight.dim() != 2 or x.dim() < 1 or x.shape[-1] != weight.shape[1]:
+        raise E.EcasqError(f"x [..., k] and weight [n, k] do not match: {list(x.shape)}, {list(weight.shape)}")
+    return _CheckpointLinear.apply(x, weight, bias, seed)

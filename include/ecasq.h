@@ -321,6 +321,83 @@ int ecasq_rans_decode(const uint16_t* words, const int32_t* seg_len, const int64
                       int two_codes, int n, int64_t d, int s, uint64_t seed, uint8_t* idx, int32_t* status,
                       void* stream);
 
+/* ---- 8-bit operators: integer linear layer, activation checkpoints ----
+ *
+ * Matrices here have their own row pitch (ld*, in elements); the elements of a
+ * row are adjacent. Element types: ECASQ_F32, ECASQ_BF16, ECASQ_F16. Row counts
+ * may be 0 (nothing is launched, except that a weight gradient over no tokens
+ * is written as zeros). These calls serve any stream of the current device and
+ * share nothing between calls, so calls may overlap and may be captured into
+ * graphs. The tensor-core kernels bound every wait for their own copies; see
+ * ecasq_device_stalled. */
+#define ECASQ_F32 0
+#define ECASQ_BF16 1
+#define ECASQ_F16 2
+
+/* Rows of X in 8-bit integers, one scale per row (a token of activations, an
+ * output channel of weights): with a = max |X[r]|, q[r][j] is the integer
+ * nearest to 127 X[r][j] / a (ties to even; the exact quotient decides) and
+ * scale[r] = a / 127 rounded to float32, so X[r][j] ~ q[r][j] * scale[r].
+ * A row of zeros has q = 0 and scale 0. A row holding a NaN or an infinity has
+ * q = 0, scale NaN and status[r] = ECASQ_ERR_RANGE. ldq is a multiple of 16, q
+ * 16-byte aligned; bytes of q between k and ldq are not written. */
+int ecasq_int8_quantize(const void* X, int x_type, int64_t n, int64_t k, int64_t ldx, int8_t* q, int64_t ldq,
+                        float* scale, int32_t* status, void* stream);
+
+/* Product of 8-bit integers with a scale per token and per output channel:
+ *   Y[i][j] = (sum_l A[i][l] B[j][l]) * sa[i] * sb[j] + bias[j],
+ * A [m][k] (tokens), B [n][k] (output channels), bias [n] float32 or NULL. The
+ * integer sum is exact (32 bits: k <= 131072), the scales are applied in
+ * float32 and the result is rounded once to y_type. lda, ldb are multiples of
+ * 16 and A, B 16-byte aligned. */
+int ecasq_int8_matmul(const int8_t* A, int64_t lda, const float* sa, const int8_t* B, int64_t ldb, const float* sb,
+                      const float* bias, int64_t m, int64_t n, int64_t k, void* Y, int y_type, int64_t ldy,
+                      void* stream);
+
+/* Activation checkpoint in 8 bits. Each row of X [t][k] is cut into blocks of
+ * 32 entries (the last one may be short); a block's scale s is the smallest
+ * power of two, at least 2^-126, with max |x| <= 127 s, stored as the byte b
+ * with s = 2^(b - 127). Each |x| / s is rounded to one of its two neighbouring
+ * integers: with f its fractional part, up iff u < nearest(65536 f) (ties to
+ * even), u 16 random bits, so E[q s] = x up to 2^-17 of s (exactly for bfloat16
+ * entries of at least 2^-9 s). u of entry j of row r is half j & 1 (low half
+ * first) of word (j >> 1) & 3 of the Philox4x32-10 block with counter
+ * (j >> 3, r, 2, 0) and the key of ecasq_encode, from seed + *seed_add
+ * (seed_add is a device pointer or NULL: a captured call draws new bits on each
+ * replay when the caller changes that word). A block with a NaN, an infinity or
+ * an entry above 127 * 2^121 has b = 255 and q = 0: every use of it gives NaN.
+ * A power of two makes q s exact in bfloat16, so the products of
+ * ecasq_checkpoint8_wgrad add no rounding of their own to the unbiased values.
+ * q [t][ldq]: ldq a multiple of 32, at least k; a row's last block is written
+ * whole, with zeros beyond k. scale [t][lds]: lds a multiple of 16, at least
+ * ceil(k / 32); bytes beyond the blocks are not written. q and scale are
+ * 16-byte aligned. */
+int ecasq_checkpoint8(const void* X, int x_type, int64_t t, int64_t k, int64_t ldx, uint64_t seed,
+                      const uint64_t* seed_add, int8_t* q, int64_t ldq, uint8_t* scale, int64_t lds, void* stream);
+
+/* The values of a checkpoint, q s, rounded to x_type (exact in float32 and
+ * bfloat16; in float16 values beyond +-65504 become +-65504). */
+int ecasq_checkpoint8_restore(const int8_t* q, int64_t ldq, const uint8_t* scale, int64_t lds, int64_t t, int64_t k,
+                              void* X, int x_type, int64_t ldx, void* stream);
+
+/* Weight gradient of a linear layer Y = X W^T from the checkpoint of X:
+ *   dW[i][j] = sum_r dY[r][i] s[r][j / 32] q[r][j],  dY [t][o], dW [o][k].
+ * Products are exact (a float16 or float32 dY is taken apart into two or three
+ * bfloat16 terms whose sum it is), sums are float32, the result is rounded once
+ * to dw_type. Long sums over few output entries are split over the tokens and
+ * joined in a fixed order, so results repeat. Workspace:
+ * ecasq_checkpoint8_wgrad_workspace_size for the same sizes, types and pitch on
+ * the current device; it may be 0. */
+size_t ecasq_checkpoint8_wgrad_workspace_size(int64_t t, int64_t o, int64_t k, int dy_type, int64_t ldy);
+int ecasq_checkpoint8_wgrad(const void* dY, int dy_type, int64_t ldy, const int8_t* q, int64_t ldq,
+                            const uint8_t* scale, int64_t lds, int64_t t, int64_t o, int64_t k, void* dW, int dw_type,
+                            int64_t ldw, void* ws, size_t ws_bytes, void* stream);
+
+/* Whether a bounded wait of the tensor-core kernels above gave up on the
+ * current device since the last call (their outputs are then invalid). Waits
+ * for the device; returns ECASQ_OK, or ECASQ_ERR_CUDA and clears the mark. */
+int ecasq_device_stalled(void);
+
 /* Static text for a status code. */
 const char* ecasq_status_string(int code);
 
