@@ -553,6 +553,10 @@ int ecasq_checkpoint8_wgrad(const void* dY, int dy_type, int64_t ldy, const int8
                                               static_cast<cudaStream_t>(stream)));
 }
 
-int ecasq_device_stalled(void) { return ECASQ_OK; }
+int ecasq_device_stalled(void) {
+  bool int8 = false;
+  if (int8_stalled(&int8) != cudaSuccess) return ECASQ_ERR_CUDA;
+  return int8 ? ECASQ_ERR_CUDA : ECASQ_OK;
+}
 
 }  // extern "C"

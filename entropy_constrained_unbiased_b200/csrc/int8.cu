@@ -2,11 +2,13 @@
 // scale per token and per output channel (include/ecasq.h, "8-bit operators").
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cstdint>
 
 #include "common.cuh"
 #include "kernels.cuh"
 #include "rows8.cuh"
+#include "tensor.cuh"
 
 namespace ecasq {
 
@@ -118,45 +120,391 @@ cudaError_t int8_rows(const void* X, int64_t n, int64_t k, int64_t ldx, int8_t* 
 }
 
 // ---- product ---------------------------------------------------------------------
+//
+// tcgen05.mma kind::i8 (int32 accumulators in TMEM: the sum is exact). The output
+// channels are the M side of the MMA and the tokens its N side, so one token costs a
+// 16-column tile instead of a 128-row one, and a thread of the epilogue owns one
+// channel: its scale and bias are read once, the 32 lanes of a warp write 32
+// adjacent outputs of a token, and outputs of any pitch or alignment are served by
+// the same stores. Operand rows come through TMA in 128-byte pieces of k (zeros
+// beyond the sizes).
 
+__device__ int g_stalled_int8;  // set when a bounded wait gave up
+
+constexpr int kPieceK = 128;  // bytes of k per stage
+constexpr int kStepK = 32;    // k of one MMA
+
+struct Product {
+  const float* sa;
+  const float* sb;
+  const float* bias;
+  void* Y;
+  int64_t m, n, ldy;
+  int pieces;  // ceil(k / 128)
+};
+
+// One output: the exact integer sum, scaled.
 template <int kType>
-__global__ void __launch_bounds__(256)
-    k_int8_matmul_plain(const int8_t* __restrict__ A, int64_t lda, const float* __restrict__ sa,
-                        const int8_t* __restrict__ B, int64_t ldb, const float* __restrict__ sb,
-                        const float* __restrict__ bias, int64_t m, int64_t n, int64_t k,
-                        typename Elem<kType>::T* __restrict__ Y, int64_t ldy) {
-  __shared__ int ta[64][17], tb[64][17];
-  const int64_t i0 = static_cast<int64_t>(blockIdx.x) * 64, j0 = static_cast<int64_t>(blockIdx.y) * 64;
-  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-  int acc[4][4] = {};
-  for (int64_t l0 = 0; l0 < k; l0 += 64) {
-    for (int e = threadIdx.x; e < 64 * 16; e += 256) {
-      const int r = e >> 4, w = e & 15;
-      int a = 0, b = 0;
-      for (int t = 0; t < 4; ++t) {
-        const int64_t l = l0 + 4 * w + t;
-        if (l < k && i0 + r < m) a |= (A[(i0 + r) * lda + l] & 0xff) << (8 * t);
-        if (l < k && j0 + r < n) b |= (B[(j0 + r) * ldb + l] & 0xff) << (8 * t);
-      }
-      ta[r][w] = a;
-      tb[r][w] = b;
+__device__ __forceinline__ void put_output(const Product& p, int64_t token, int64_t channel, int acc, float a, float s,
+                                           float bias) {
+  static_cast<typename Elem<kType>::T*>(p.Y)[token * p.ldy + channel] =
+      Elem<kType>::put(fmaf(static_cast<float>(acc) * a, s, bias));
+}
+
+// -- few tokens: a tile of 128 channels by kTok tokens per cluster, k split over the
+// cluster's CTAs and joined through distributed shared memory (integers: the order
+// does not matter) --
+
+template <int kTok>
+struct TileCfg {
+  static constexpr int kA = 128 * kPieceK, kB = kTok * kPieceK;
+  static constexpr int kStages = kTok <= 64 ? 4 : 3;
+  static constexpr int kJoin = kTok * 128 * 4;  // partial sums, over the stages
+  static constexpr int kTiles = kStages * (kA + kB) > kJoin ? kStages * (kA + kB) : kJoin;
+  static constexpr int kSmem = kTiles + 1024;
+  static constexpr int kColumns = kTok < 32 ? 32 : kTok;
+};
+
+template <int kType, int kTok>
+__global__ void __launch_bounds__(192, 2)
+    k_int8_tile(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_x, const Product p,
+                int channel_tiles, int split) {
+  using Cfg = TileCfg<kTok>;
+  extern __shared__ unsigned char smem_raw[];
+  __shared__ uint64_t bars[2 * Cfg::kStages + 1];
+  __shared__ uint32_t tmem_slot;
+  const uint32_t tiles = (smem_addr(smem_raw) + 1023) & ~1023u;
+  const uint32_t full = smem_addr(bars), empty = full + 8 * Cfg::kStages, done = empty + 8 * Cfg::kStages;
+  const int warp = warp_id(), lane = lane_id();
+  const int tile = static_cast<int>(blockIdx.x) / split;
+  const int part = static_cast<int>(blockIdx.x) % split;
+  const int channel0 = (tile % channel_tiles) * 128;
+  const int token0 = (tile / channel_tiles) * kTok;
+  const int per = (p.pieces + split - 1) / split;
+  const int first = part * per;
+  const int count = min(p.pieces, first + per) - first;  // at least 1 (the host's choice of split)
+
+  if (warp == 4) tmem_alloc<1>(smem_addr(&tmem_slot), Cfg::kColumns);
+  if (threadIdx.x == 0) {
+    prefetch_map(&map_w);
+    prefetch_map(&map_x);
+    for (int i = 0; i < Cfg::kStages; ++i) {
+      mbar_init(full + 8 * i, 1);
+      mbar_init(empty + 8 * i, 1);
     }
-    __syncthreads();
-    for (int w = 0; w < 16; ++w)
+    mbar_init(done, 1);
+    fence_mbar_init();
+  }
+  tcgen05_before_sync();
+  __syncthreads();
+  tcgen05_after_sync();
+  const uint32_t acc = tmem_slot;
+  bool ok = true;
+
+  if (warp == 4) {
+    if (lane == 0) {
+      int loaded = 0;
+      for (; loaded < count && ok; ++loaded) {
+        const int s = loaded % Cfg::kStages;
+        if (loaded >= Cfg::kStages) {
+          ok = mbar_wait_bounded(empty + 8 * s, (loaded / Cfg::kStages + 1) & 1, kWaitLimit);
+          if (!ok) break;
+        }
+        const uint32_t a = tiles + s * (Cfg::kA + Cfg::kB);
+        mbar_expect_tx(full + 8 * s, Cfg::kA + Cfg::kB);
+        tma_2d(a, &map_w, (first + loaded) * kPieceK, channel0, full + 8 * s);
+        tma_2d(a + Cfg::kA, &map_x, (first + loaded) * kPieceK, token0, full + 8 * s);
+      }
+      if (!ok)  // wait for the copies in flight before the memory is given back
+        for (int i = max(0, loaded - Cfg::kStages); i < loaded; ++i)
+          mbar_wait_bounded(full + 8 * (i % Cfg::kStages), (i / Cfg::kStages) & 1, kWaitLimit);
+    }
+  } else if (warp == 5) {
+    if (lane == 0) {
+      for (int i = 0; i < count && ok; ++i) {
+        const int s = i % Cfg::kStages;
+        ok = mbar_wait_bounded(full + 8 * s, (i / Cfg::kStages) & 1, kWaitLimit);
+        if (!ok) break;
+        tcgen05_after_sync();
+        const uint32_t a = tiles + s * (Cfg::kA + Cfg::kB);
+        const uint64_t da = smem_desc(a, 16, 1024), db = smem_desc(a + Cfg::kA, 16, 1024);
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
+        for (int j = 0; j < kPieceK / kStepK; ++j)
+          mma_i8<1>(acc, da + j * (kStepK >> 4), db + j * (kStepK >> 4), idesc_i8(128, kTok), i > 0 || j > 0);
+        mma_commit<1>(empty + 8 * s);
+      }
+      mma_commit<1>(done);
+    }
+  } else {
+    ok = mbar_wait_bounded(done, 0, kWaitLimit);
+    tcgen05_after_sync();
+    const int64_t channel = channel0 + warp * 32 + lane;
+    const int tokens = static_cast<int>(min(static_cast<int64_t>(kTok), p.m - token0));
+    const bool live = ok && channel < p.n;
+    const float s = live && split == 1 ? p.sb[channel] : 0.0f;
+    const float bias = live && split == 1 && p.bias ? p.bias[channel] : 0.0f;
+    constexpr int kCols = kTok < 32 ? 16 : 32;
+    for (int j0 = 0; j0 < tokens; j0 += kCols) {
+      uint32_t v[kCols];
+      const uint32_t at = acc + (static_cast<uint32_t>(warp) << 21) + j0;  // lane 32 * warp in bits 16 and up
+      if constexpr (kCols == 16)
+        tmem_ld16(at, v);
+      else
+        tmem_ld32(at, v);
+      tcgen05_wait_ld();
+      if (split == 1) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) acc[i][j] = __dp4a(ta[ty + 16 * i][w], tb[tx + 16 * j][w], acc[i][j]);
+        for (int j = 0; j < kCols; ++j)
+          if (live && j0 + j < tokens)
+            put_output<kType>(p, token0 + j0 + j, channel, static_cast<int>(v[j]), __ldg(p.sa + token0 + j0 + j), s, bias);
+      } else {
+#pragma unroll
+        for (int j = 0; j < kCols; ++j)
+          if (j0 + j < tokens)
+            asm volatile("st.shared.b32 [%0], %1;" ::"r"(tiles + 4 * ((j0 + j) * 128 + warp * 32 + lane)), "r"(v[j])
+                         : "memory");
+      }
+    }
+    tcgen05_before_sync();
+  }
+  if (!ok) g_stalled_int8 = 1;
+  __syncwarp();
+  if (split > 1) {
+    cluster_sync_all();
+    if (warp < 4) {
+      const int64_t channel = channel0 + warp * 32 + lane;
+      const int tokens = static_cast<int>(min(static_cast<int64_t>(kTok), p.m - token0));
+      if (channel < p.n) {
+        const float s = p.sb[channel], bias = p.bias ? p.bias[channel] : 0.0f;
+        for (int j = part; j < tokens; j += split) {
+          int sum = 0;
+          for (int r = 0; r < split; ++r)
+            sum += ld_shared_cluster(map_shared(tiles + 4 * (j * 128 + warp * 32 + lane), r));
+          put_output<kType>(p, token0 + j, channel, sum, __ldg(p.sa + token0 + j), s, bias);
+        }
+      }
+    }
+    cluster_sync_all();  // the partial sums stay until every CTA has read them
+  } else {
     __syncthreads();
   }
-  for (int i = 0; i < 4; ++i)
-    for (int j = 0; j < 4; ++j) {
-      const int64_t r = i0 + ty + 16 * i, c = j0 + tx + 16 * j;
-      if (r < m && c < n) {
-        const float y = static_cast<float>(acc[i][j]) * sa[r] * sb[c];
-        Y[r * ldy + c] = Elem<kType>::put(bias ? y + bias[c] : y);
+  if (warp == 4) {
+    tcgen05_after_sync();
+    tmem_free<1>(acc, Cfg::kColumns);
+  }
+}
+
+template <int kType, int kTok>
+cudaError_t int8_tile(const CUtensorMap& map_w, const CUtensorMap& map_x, const Product& p, int split, cudaStream_t st) {
+  using Cfg = TileCfg<kTok>;
+  const cudaError_t e = cudaFuncSetAttribute(k_int8_tile<kType, kTok>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::kSmem);
+  if (e != cudaSuccess) return e;
+  const int channel_tiles = static_cast<int>((p.n + 127) / 128);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(channel_tiles * ((p.m + kTok - 1) / kTok) * split));
+  cfg.blockDim = dim3(192);
+  cfg.dynamicSmemBytes = Cfg::kSmem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = static_cast<unsigned>(split);
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  note_launch();
+  return cudaLaunchKernelEx(&cfg, k_int8_tile<kType, kTok>, map_w, map_x, p, channel_tiles, split);
+}
+
+// -- many tokens: a pair of CTAs (cta_group::2) per 256 channels by 256 tokens,
+// persistent over the tiles, the accumulators of one tile written out while the next
+// one is computed --
+
+constexpr int kPairStages = 6;
+constexpr int kPairStage = 2 * 128 * kPieceK;  // each CTA: 128 rows of either operand
+constexpr int kPairSmem = kPairStages * kPairStage + 1024;
+
+// The tile order: blocks of up to 16 channel tiles, token tiles within a block, so
+// that the operand rows that CTAs share at one time stay in L2.
+struct TileAt {
+  int channel, token;
+};
+__device__ __forceinline__ TileAt tile_at(int t, int channel_tiles, int token_tiles) {
+  const int block = t / (16 * token_tiles), in = t - block * 16 * token_tiles;
+  const int width = min(16, channel_tiles - 16 * block);
+  return {16 * block + in % width, in / width};
+}
+
+template <int kType>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(192, 1)
+    k_int8_pair(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_x, const Product p,
+                int channel_tiles, int token_tiles) {
+  extern __shared__ unsigned char smem_raw[];
+  __shared__ uint64_t bars[2 * kPairStages + 4];
+  __shared__ uint32_t tmem_slot;
+  __shared__ float token_scale[2][256];
+  const uint32_t tiles = (smem_addr(smem_raw) + 1023) & ~1023u;
+  const uint32_t full = smem_addr(bars), empty = full + 8 * kPairStages;
+  const uint32_t done = empty + 8 * kPairStages, freed = done + 16;  // per accumulator buffer
+  const int warp = warp_id(), lane = lane_id();
+  const int rank = static_cast<int>(cluster_rank());
+  const int pair = static_cast<int>(blockIdx.x) >> 1, pairs = static_cast<int>(gridDim.x) >> 1;
+  const int all = channel_tiles * token_tiles;
+
+  if (warp == 4) tmem_alloc<2>(smem_addr(&tmem_slot), 512);
+  if (threadIdx.x == 0) {
+    prefetch_map(&map_w);
+    prefetch_map(&map_x);
+    for (int i = 0; i < kPairStages; ++i) {
+      mbar_init(full + 8 * i, 1);
+      mbar_init(empty + 8 * i, 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(done + 8 * i, 1);
+      mbar_init(freed + 8 * i, 8);  // four warps of either CTA
+    }
+    fence_mbar_init();
+  }
+  tcgen05_before_sync();
+  cluster_sync_all();
+  tcgen05_after_sync();
+  const uint32_t acc = tmem_slot;
+  bool ok = true;
+
+  if (warp == 4) {
+    if (lane == 0) {
+      const uint32_t full0 = map_shared(full, 0);
+      int64_t it = 0;
+      for (int t = pair; t < all && ok; t += pairs) {
+        const TileAt at = tile_at(t, channel_tiles, token_tiles);
+        const int c0 = at.channel * 256 + rank * 128, t0 = at.token * 256 + rank * 128;
+        for (int i = 0; i < p.pieces; ++i, ++it) {
+          const int s = static_cast<int>(it % kPairStages);
+          if (it >= kPairStages) {
+            ok = mbar_wait_bounded(empty + 8 * s, (it / kPairStages + 1) & 1, kWaitLimit);
+            if (!ok) break;
+          }
+          const uint32_t a = tiles + s * kPairStage;
+          if (rank == 0) mbar_expect_tx(full + 8 * s, 2 * kPairStage);
+          tma_2d_pair(a, &map_w, i * kPieceK, c0, full0 + 8 * s);
+          tma_2d_pair(a + 128 * kPieceK, &map_x, i * kPieceK, t0, full0 + 8 * s);
+        }
+      }
+      if (!ok && rank == 0)
+        for (int64_t i = it > kPairStages ? it - kPairStages : 0; i < it; ++i)
+          mbar_wait_bounded(full + 8 * static_cast<uint32_t>(i % kPairStages), (i / kPairStages) & 1, kWaitLimit);
+    }
+  } else if (warp == 5) {
+    if (lane == 0 && rank == 0) {
+      int64_t it = 0;
+      int n = 0;
+      for (int t = pair; t < all && ok; t += pairs, ++n) {
+        const int buf = n & 1;
+        if (n >= 2) {
+          ok = mbar_wait_bounded(freed + 8 * buf, ((n >> 1) + 1) & 1, kWaitLimit);
+          if (!ok) break;
+        }
+        tcgen05_after_sync();
+        for (int i = 0; i < p.pieces; ++i, ++it) {
+          const int s = static_cast<int>(it % kPairStages);
+          ok = mbar_wait_bounded(full + 8 * s, (it / kPairStages) & 1, kWaitLimit);
+          if (!ok) break;
+          tcgen05_after_sync();
+          const uint32_t a = tiles + s * kPairStage;
+          const uint64_t da = smem_desc(a, 16, 1024), db = smem_desc(a + 128 * kPieceK, 16, 1024);
+#pragma unroll
+          for (int j = 0; j < kPieceK / kStepK; ++j)
+            mma_i8<2>(acc + buf * 256, da + j * (kStepK >> 4), db + j * (kStepK >> 4), idesc_i8(256, 256), i > 0 || j > 0);
+          mma_commit<2>(empty + 8 * s);
+        }
+        mma_commit<2>(done + 8 * buf);
       }
     }
+  } else {
+    int n = 0;
+    for (int t = pair; t < all; t += pairs, ++n) {
+      const int buf = n & 1;
+      const TileAt at = tile_at(t, channel_tiles, token_tiles);
+      const int64_t channel = static_cast<int64_t>(at.channel) * 256 + rank * 128 + warp * 32 + lane;
+      const int64_t token0 = static_cast<int64_t>(at.token) * 256;
+      const int tokens = static_cast<int>(min(static_cast<int64_t>(256), p.m - token0));
+      for (int j = threadIdx.x; j < tokens; j += 128) token_scale[buf][j] = p.sa[token0 + j];
+      const bool live = channel < p.n;
+      const float s = live ? p.sb[channel] : 0.0f;
+      const float bias = live && p.bias ? p.bias[channel] : 0.0f;
+      asm volatile("bar.sync 1, 128;" ::: "memory");
+      ok = __all_sync(0xffffffffu, mbar_wait_bounded(done + 8 * buf, (n >> 1) & 1, kWaitLimit));
+      if (!ok) break;
+      tcgen05_after_sync();
+      for (int j0 = 0; j0 < tokens; j0 += 32) {
+        uint32_t v[32];
+        tmem_ld32(acc + (static_cast<uint32_t>(warp) << 21) + buf * 256 + j0, v);
+        tcgen05_wait_ld();
+        if (live) {
+#pragma unroll
+          for (int j = 0; j < 32; ++j)
+            if (j0 + j < tokens)
+              put_output<kType>(p, token0 + j0 + j, channel, static_cast<int>(v[j]), token_scale[buf][j0 + j], s, bias);
+        }
+      }
+      tcgen05_before_sync();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cluster(map_shared(freed + 8 * buf, 0));
+    }
+  }
+  if (!ok) g_stalled_int8 = 1;
+  __syncwarp();
+  tcgen05_before_sync();
+  cluster_sync_all();  // neither CTA leaves while the other's MMAs or copies use its memory
+  if (warp == 4) {
+    tcgen05_after_sync();
+    tmem_free<2>(acc, 512);
+  }
+}
+
+template <int kType>
+cudaError_t int8_pair(const CUtensorMap& map_w, const CUtensorMap& map_x, const Product& p, cudaStream_t st) {
+  const cudaError_t e = cudaFuncSetAttribute(k_int8_pair<kType>, cudaFuncAttributeMaxDynamicSharedMemorySize, kPairSmem);
+  if (e != cudaSuccess) return e;
+  const int64_t channel_tiles = (p.n + 255) / 256, token_tiles = (p.m + 255) / 256;
+  if (channel_tiles * token_tiles > INT32_MAX / 32) return cudaErrorInvalidValue;
+  const int pairs = static_cast<int>(std::min<int64_t>(sm_count() / 2, channel_tiles * token_tiles));
+  k_int8_pair<kType><<<2 * pairs, 192, kPairSmem, st>>>(map_w, map_x, p, static_cast<int>(channel_tiles),
+                                                       static_cast<int>(token_tiles));
+  note_launch();
+  return cudaGetLastError();
+}
+
+// A map of 8-bit rows in boxes of 128 bytes by `rows`.
+bool map_rows8(CUtensorMap* map, const int8_t* p, int64_t n, int64_t k, int64_t ld, int rows) {
+  const uint64_t sizes[2] = {static_cast<uint64_t>(k), static_cast<uint64_t>(n)}, strides[1] = {static_cast<uint64_t>(ld)};
+  const uint32_t box[2] = {kPieceK, static_cast<uint32_t>(rows)};
+  return make_map(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, p, sizes, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
+template <int kType, int kTok>
+cudaError_t int8_few(const int8_t* A, int64_t lda, const int8_t* B, int64_t ldb, const Product& p, int64_t k,
+                     cudaStream_t st) {
+  CUtensorMap map_w, map_x;
+  if (!map_rows8(&map_w, B, p.n, k, ldb, 128) || !map_rows8(&map_x, A, p.m, k, lda, kTok)) return cudaErrorInvalidValue;
+  const int64_t tiles = (p.n + 127) / 128 * ((p.m + kTok - 1) / kTok);
+  if (tiles > INT32_MAX / 16) return cudaErrorInvalidValue;
+  // split k until the CTAs fill the GPU (two per SM), with at least two pieces each
+  int split = 1;
+  while (split < 8 && tiles * split * 2 <= 2 * sm_count() && p.pieces >= 4 * split) split *= 2;
+  while (split > 1 && (split - 1) * ((p.pieces + split - 1) / split) >= p.pieces) split /= 2;
+  return int8_tile<kType, kTok>(map_w, map_x, p, split, st);
+}
+
+template <int kType>
+cudaError_t int8_product(const int8_t* A, int64_t lda, const int8_t* B, int64_t ldb, const Product& p, int64_t k,
+                         cudaStream_t st) {
+  if (p.m <= 16) return int8_few<kType, 16>(A, lda, B, ldb, p, k, st);
+  if (p.m <= 32) return int8_few<kType, 32>(A, lda, B, ldb, p, k, st);
+  if (p.m <= 64) return int8_few<kType, 64>(A, lda, B, ldb, p, k, st);
+  if (p.m <= 256) return int8_few<kType, 128>(A, lda, B, ldb, p, k, st);
+  CUtensorMap map_w, map_x;
+  if (!map_rows8(&map_w, B, p.n, k, ldb, 128) || !map_rows8(&map_x, A, p.m, k, lda, 128)) return cudaErrorInvalidValue;
+  return int8_pair<kType>(map_w, map_x, p, st);
 }
 
 }  // namespace
@@ -173,16 +521,23 @@ cudaError_t launch_int8_quantize(const void* X, int type, int64_t n, int64_t k, 
 cudaError_t launch_int8_matmul(const int8_t* A, int64_t lda, const float* sa, const int8_t* B, int64_t ldb,
                                const float* sb, const float* bias, int64_t m, int64_t n, int64_t k, void* Y, int type,
                                int64_t ldy, cudaStream_t st) {
-  const dim3 grid(static_cast<unsigned>((m + 63) / 64), static_cast<unsigned>((n + 63) / 64));
-  if (type == kF32)
-    k_int8_matmul_plain<kF32><<<grid, 256, 0, st>>>(A, lda, sa, B, ldb, sb, bias, m, n, k, static_cast<float*>(Y), ldy);
-  else if (type == kBF16)
-    k_int8_matmul_plain<kBF16>
-        <<<grid, 256, 0, st>>>(A, lda, sa, B, ldb, sb, bias, m, n, k, static_cast<__nv_bfloat16*>(Y), ldy);
-  else
-    k_int8_matmul_plain<kF16><<<grid, 256, 0, st>>>(A, lda, sa, B, ldb, sb, bias, m, n, k, static_cast<__half*>(Y), ldy);
-  note_launch();
-  return cudaGetLastError();
+  const Product p = {sa, sb, bias, Y, m, n, ldy, static_cast<int>((k + kPieceK - 1) / kPieceK)};
+  switch (type) {
+    case kF32: return int8_product<kF32>(A, lda, B, ldb, p, k, st);
+    case kBF16: return int8_product<kBF16>(A, lda, B, ldb, p, k, st);
+    default: return int8_product<kF16>(A, lda, B, ldb, p, k, st);
+  }
+}
+
+cudaError_t int8_stalled(bool* stalled) {
+  int v = 0;
+  cudaError_t e = cudaMemcpyFromSymbol(&v, g_stalled_int8, sizeof(v));
+  *stalled = v != 0;
+  if (e == cudaSuccess && v) {
+    v = 0;
+    e = cudaMemcpyToSymbol(g_stalled_int8, &v, sizeof(v));
+  }
+  return e;
 }
 
 }  // namespace ecasq
