@@ -535,9 +535,10 @@ int ecasq_checkpoint8_restore(const int8_t* q, int64_t ldq, const uint8_t* scale
       launch_checkpoint8_restore(q, ldq, scale, lds, t, k, X, x_type, ldx, static_cast<cudaStream_t>(stream)));
 }
 
-size_t ecasq_checkpoint8_wgrad_workspace_size(int64_t t, int64_t o, int64_t k, int dy_type, int64_t ldy) {
+size_t ecasq_checkpoint8_wgrad_workspace_size(const void* dY, int dy_type, int64_t ldy, int64_t t, int64_t o,
+                                              int64_t k) {
   if (!valid_type(dy_type) || !valid_rows(t, k) || o < 1 || o > kMaxCols8) return 0;
-  return checkpoint8_wgrad_workspace(t, o, k, dy_type, ldy);
+  return checkpoint8_wgrad_workspace(dY, dy_type, ldy, t, o, k);
 }
 
 int ecasq_checkpoint8_wgrad(const void* dY, int dy_type, int64_t ldy, const int8_t* q, int64_t ldq,
@@ -547,16 +548,16 @@ int ecasq_checkpoint8_wgrad(const void* dY, int dy_type, int64_t ldy, const int8
     return ECASQ_ERR_ARG;
   if (!dW || !valid_pitch(o, k, ldw)) return ECASQ_ERR_ARG;
   if (t > 0 && (!dY || !valid_pitch(t, o, ldy) || !valid_checkpoint(q, ldq, scale, lds, k))) return ECASQ_ERR_ARG;
-  const size_t need = checkpoint8_wgrad_workspace(t, o, k, dy_type, ldy);
+  const size_t need = checkpoint8_wgrad_workspace(dY, dy_type, ldy, t, o, k);
   if (need && (!ws || ws_bytes < need)) return ECASQ_ERR_WORKSPACE;
   return cuda_status(launch_checkpoint8_wgrad(dY, dy_type, ldy, q, ldq, scale, lds, t, o, k, dW, dw_type, ldw, ws,
                                               static_cast<cudaStream_t>(stream)));
 }
 
 int ecasq_device_stalled(void) {
-  bool int8 = false;
-  if (int8_stalled(&int8) != cudaSuccess) return ECASQ_ERR_CUDA;
-  return int8 ? ECASQ_ERR_CUDA : ECASQ_OK;
+  bool int8 = false, checkpoint = false;
+  if (int8_stalled(&int8) != cudaSuccess || checkpoint8_stalled(&checkpoint) != cudaSuccess) return ECASQ_ERR_CUDA;
+  return int8 || checkpoint ? ECASQ_ERR_CUDA : ECASQ_OK;
 }
 
 }  // extern "C"

@@ -2,11 +2,13 @@
 // (include/ecasq.h, "8-bit operators").
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cstdint>
 
 #include "common.cuh"
 #include "kernels.cuh"
 #include "rows8.cuh"
+#include "tensor.cuh"
 
 namespace ecasq {
 
@@ -102,49 +104,419 @@ void piece_grid(int64_t t, int64_t pieces, dim3* grid, dim3* block) {
   *grid = dim3(static_cast<unsigned>((t + block->y - 1) / block->y), static_cast<unsigned>((pieces + x - 1) / x));
 }
 
-template <int kIn, int kOut>
-__global__ void __launch_bounds__(256)
-    k_wgrad_plain(const typename Elem<kIn>::T* __restrict__ dY, int64_t ldy, const int8_t* __restrict__ Q, int64_t ldq,
-                  const uint8_t* __restrict__ S, int64_t lds, int64_t t, int64_t o, int64_t k,
-                  typename Elem<kOut>::T* __restrict__ dW, int64_t ldw) {
-  __shared__ float ta[16][65], tb[16][65];
-  const int64_t i0 = static_cast<int64_t>(blockIdx.x) * 64, j0 = static_cast<int64_t>(blockIdx.y) * 64;
-  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-  float acc[4][4] = {};
-  for (int64_t r0 = 0; r0 < t; r0 += 16) {
-    for (int e = threadIdx.x; e < 16 * 64; e += 256) {
-      const int64_t r = r0 + (e >> 6), i = i0 + (e & 63), j = j0 + (e & 63);
-      ta[e >> 6][e & 63] = r < t && i < o ? Elem<kIn>::get(dY[r * ldy + i]) : 0.0f;
-      tb[e >> 6][e & 63] =
-          r < t && j < k ? static_cast<float>(Q[r * ldq + j]) * scale_value(S[r * lds + j / 32]) : 0.0f;
-    }
-    __syncthreads();
-    for (int w = 0; w < 16; ++w)
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) acc[i][j] += ta[w][ty + 16 * i] * tb[w][tx + 16 * j];
-    __syncthreads();
-  }
-  for (int i = 0; i < 4; ++i)
-    for (int j = 0; j < 4; ++j) {
-      const int64_t r = i0 + ty + 16 * i, c = j0 + tx + 16 * j;
-      if (r < o && c < k) dW[r * ldw + c] = Elem<kOut>::put(acc[i][j]);
-    }
+// ---- weight gradient -------------------------------------------------------------
+//
+// dW = dY^T X^ with tcgen05.mma kind::f16 (bf16 operands, float32 accumulators in
+// TMEM). X^ = q s is exact in bf16 (8 bits times a power of two) and is made from
+// the checkpoint on its way to the tensor cores: warps read the integers from the
+// stage that TMA filled and write bf16 into the operand's shared memory, once for
+// all terms of dY. Both operands lie token by token, so both are M- or N-contiguous
+// ("MN-major") and nothing is transposed. The features of X are the M side: a
+// thread of the epilogue owns one feature and the 32 lanes of a warp write 32
+// adjacent entries of a row of dW. A pair of CTAs (cta_group::2) takes 256 features
+// by 256 outputs; each CTA converts its own 128 features only.
+//
+// The tensor core adds to its float32 accumulator by cutting, not rounding: a step of
+// 16 tokens loses up to 2^-23 of the running sum, always towards zero, and n steps
+// about 2.3e-8 n of it (measured: 2.2e-6 after 96). That is far below a bfloat16
+// result's own rounding (2^-9 on average), and one accumulator takes the whole sum. For float32
+// and float16 results (kExact) an accumulator takes 16 steps or so, and the epilogue
+// warps add it, rounding to nearest, to sums that they hold in registers.
+
+__device__ int g_stalled_checkpoint8;  // set when a bounded wait gave up
+
+constexpr int kTok = 64;                  // tokens per stage
+constexpr int kOperand = kTok * 128 * 2;  // bf16 operand of one CTA: 128 features, or 128 outputs
+constexpr int kHalf = kTok * 64 * 2;      // its 64-wide half (one swizzle atom across)
+constexpr int kInts = kTok * 128;         // integers of 128 features
+constexpr int kScales = kTok * 16;        // scale bytes of 512 features
+constexpr int kXStage = kOperand + kInts + kScales;
+constexpr int kXStages = 4, kYStages = 7;
+constexpr int kGradSmem = kXStages * kXStage + kYStages * kOperand + 1024;
+
+// Warps: the epilogue's, the producer, the MMA issuer, the converters. kExact holds
+// 128 sums a thread in the epilogue's registers, so its warps come in groups of four
+// that trade registers (setmaxnreg): 256 * 184 + 256 * 72 = 512 * 128.
+template <bool kExact>
+struct GradWarps {
+  static constexpr int kEpilogue = kExact ? 8 : 4;
+  static constexpr int kLoad = kEpilogue, kIssue = kEpilogue + 1;
+  static constexpr int kConvert0 = kExact ? 12 : 6;
+  static constexpr int kConvert = kExact ? 4 : 8;
+  static constexpr int kThreads = 32 * (kConvert0 + kConvert);
+};
+
+struct Gradient {
+  void* out;          // dW, or the partial sums when the tokens are split
+  int64_t o, k, ld;   // size and pitch of one output matrix
+  int feature_tiles, output_tiles;
+  int pieces;         // ceil(t / 64)
+  int terms;          // bf16 terms of dY, the smallest first
+  int split, per;     // parts of the token axis, pieces of one
+  int chunk;          // pieces that one accumulator takes
+};
+
+// Two bytes of x as two's complement integers times s, in bf16. 0x4300 | b is the bf16
+// number 128 + (b & 127) with bit 7 cleared, and 128 or 256 with the low bits
+// cleared; their difference is the integer, exactly.
+__device__ __forceinline__ uint32_t two_values(uint32_t x, uint32_t selector, __nv_bfloat162 s) {
+  const uint32_t h = __byte_perm(x, 0x43434343u, selector);
+  const uint32_t low = h & 0xFF7FFF7Fu, high = h & 0xFF80FF80u;
+  const __nv_bfloat162 v = __hmul2(
+      __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&low), *reinterpret_cast<const __nv_bfloat162*>(&high)), s);
+  return *reinterpret_cast<const uint32_t*>(&v);
 }
 
-template <int kIn>
-cudaError_t wgrad_plain(const void* dY, int64_t ldy, const int8_t* q, int64_t ldq, const uint8_t* scale, int64_t lds,
-                        int64_t t, int64_t o, int64_t k, void* dW, int out, int64_t ldw, cudaStream_t st) {
-  const auto* y = static_cast<const typename Elem<kIn>::T*>(dY);
-  const dim3 grid(static_cast<unsigned>((o + 63) / 64), static_cast<unsigned>((k + 63) / 64));
-  if (out == kF32)
-    k_wgrad_plain<kIn, kF32><<<grid, 256, 0, st>>>(y, ldy, q, ldq, scale, lds, t, o, k, static_cast<float*>(dW), ldw);
-  else if (out == kBF16)
-    k_wgrad_plain<kIn, kBF16>
-        <<<grid, 256, 0, st>>>(y, ldy, q, ldq, scale, lds, t, o, k, static_cast<__nv_bfloat16*>(dW), ldw);
-  else
-    k_wgrad_plain<kIn, kF16><<<grid, 256, 0, st>>>(y, ldy, q, ldq, scale, lds, t, o, k, static_cast<__half*>(dW), ldw);
+__device__ __forceinline__ void st_shared16(uint32_t addr, uint4 v) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+__device__ __forceinline__ uint4 ld_shared16(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ uint32_t ld_shared1(uint32_t addr) {
+  uint32_t v;
+  asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+  return v;
+}
+
+template <int kOut, bool kExact>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GradWarps<kExact>::kThreads, 1)
+    k_wgrad(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_s,
+            const __grid_constant__ CUtensorMap map_y, const Gradient g) {
+  using W = GradWarps<kExact>;
+  extern __shared__ unsigned char smem_raw[];
+  __shared__ uint64_t bars[3 * kXStages + 2 * kYStages + 4];
+  __shared__ uint32_t tmem_slot;
+  const uint32_t xs = (smem_addr(smem_raw) + 1023) & ~1023u, ys = xs + kXStages * kXStage;
+  // integers and scales here (own CTA), X^ converted (both CTAs, on the even one), X^
+  // read by the MMAs; dY here (both CTAs, on the even one), dY read; per accumulator:
+  // done, freed
+  const uint32_t ints = smem_addr(bars), ready = ints + 8 * kXStages, x_empty = ready + 8 * kXStages,
+                 full = x_empty + 8 * kXStages, y_empty = full + 8 * kYStages, done = y_empty + 8 * kYStages,
+                 freed = done + 16;
+  const int warp = warp_id(), lane = lane_id();
+  const int rank = static_cast<int>(cluster_rank());
+  const int pair = static_cast<int>(blockIdx.x) >> 1, pairs = static_cast<int>(gridDim.x) >> 1;
+  const int tiles = g.feature_tiles * g.output_tiles;
+  const int all = tiles * g.split;
+
+  if (warp == W::kLoad) tmem_alloc<2>(smem_addr(&tmem_slot), 512);
+  if (threadIdx.x == 0) {
+    prefetch_map(&map_q);
+    prefetch_map(&map_s);
+    prefetch_map(&map_y);
+    for (int i = 0; i < kXStages; ++i) {
+      mbar_init(ints + 8 * i, 1);
+      mbar_init(ready + 8 * i, 2 * W::kConvert);
+      mbar_init(x_empty + 8 * i, 1);
+    }
+    for (int i = 0; i < kYStages; ++i) {
+      mbar_init(full + 8 * i, 1);
+      mbar_init(y_empty + 8 * i, 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(done + 8 * i, 1);
+      mbar_init(freed + 8 * i, 2 * W::kEpilogue);
+    }
+    fence_mbar_init();
+  }
+  tcgen05_before_sync();
+  cluster_sync_all();
+  tcgen05_after_sync();
+  const uint32_t acc = tmem_slot;
+  bool ok = true;
+
+  if (warp >= W::kEpilogue) {
+    if constexpr (kExact) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+    if (warp == W::kLoad && lane == 0) {
+      const uint32_t full0 = map_shared(full, 0);
+      int64_t ix = 0, iy = 0;
+      for (int w = pair; w < all && ok; w += pairs) {
+        const int tile = w % tiles, part = w / tiles;
+        const int f0 = (tile % g.feature_tiles) * 256 + rank * 128, o0 = (tile / g.feature_tiles) * 256 + rank * 128;
+        const int last = min(g.pieces, (part + 1) * g.per);
+        for (int i = part * g.per; i < last && ok; ++i, ++ix) {
+          const int s = static_cast<int>(ix % kXStages);
+          if (ix >= kXStages) ok = mbar_wait_bounded(x_empty + 8 * s, (ix / kXStages + 1) & 1, kWaitLimit);
+          if (!ok) break;
+          const uint32_t q = xs + s * kXStage + kOperand;
+          mbar_expect_tx(ints + 8 * s, kInts + kScales);
+          tma_2d(q, &map_q, f0, i * kTok, ints + 8 * s);
+          tma_2d(q + kInts, &map_s, (f0 / 32) & ~15, i * kTok, ints + 8 * s);
+          for (int term = 0; term < g.terms; ++term, ++iy) {
+            const int y = static_cast<int>(iy % kYStages);
+            if (iy >= kYStages) ok = mbar_wait_bounded(y_empty + 8 * y, (iy / kYStages + 1) & 1, kWaitLimit);
+            if (!ok) break;
+            if (rank == 0) mbar_expect_tx(full + 8 * y, 2 * kOperand);
+            tma_3d_pair(ys + y * kOperand, &map_y, o0, i * kTok, term, full0 + 8 * y);
+            tma_3d_pair(ys + y * kOperand + kHalf, &map_y, o0 + 64, i * kTok, term, full0 + 8 * y);
+          }
+        }
+      }
+      if (!ok) {  // wait for the copies in flight before the memory is given back
+        for (int64_t i = ix > kXStages ? ix - kXStages : 0; i < ix; ++i)
+          mbar_wait_bounded(ints + 8 * static_cast<uint32_t>(i % kXStages), (i / kXStages) & 1, kWaitLimit);
+        for (int64_t i = iy > kYStages ? iy - kYStages : 0; i < iy && rank == 0; ++i)
+          mbar_wait_bounded(full + 8 * static_cast<uint32_t>(i % kYStages), (i / kYStages) & 1, kWaitLimit);
+      }
+    } else if (warp == W::kIssue && lane == 0 && rank == 0) {
+      int64_t ix = 0, iy = 0;
+      int n = 0;  // accumulators begun
+      for (int w = pair; w < all && ok; w += pairs) {
+        const int part = w / tiles;
+        const int count = min(g.pieces, (part + 1) * g.per) - part * g.per;
+        for (int i = 0; i < count && ok; ++n) {
+          const int buf = n & 1;
+          if (n >= 2) ok = mbar_wait_bounded(freed + 8 * buf, ((n >> 1) + 1) & 1, kWaitLimit);
+          if (!ok) break;
+          tcgen05_after_sync();
+          const int end = min(count, i + g.chunk);
+          for (bool add = false; i < end && ok; ++i, ++ix) {
+            const int s = static_cast<int>(ix % kXStages);
+            ok = mbar_wait_bounded(ready + 8 * s, (ix / kXStages) & 1, kWaitLimit);
+            const uint64_t da = smem_desc(xs + s * kXStage, kHalf, 1024);
+            for (int term = 0; term < g.terms && ok; ++term, ++iy) {
+              const int y = static_cast<int>(iy % kYStages);
+              ok = mbar_wait_bounded(full + 8 * y, (iy / kYStages) & 1, kWaitLimit);
+              if (!ok) break;
+              tcgen05_after_sync();
+              const uint64_t db = smem_desc(ys + y * kOperand, kHalf, 1024);
+#pragma unroll
+              for (int j = 0; j < kTok / 16; ++j) {  // 16 tokens per MMA: 16 rows of 128 bytes
+                mma_bf16<2>(acc + buf * 256, da + j * (2048 >> 4), db + j * (2048 >> 4), idesc_bf16_mn(256, 256), add);
+                add = true;
+              }
+              mma_commit<2>(y_empty + 8 * y);
+            }
+            mma_commit<2>(x_empty + 8 * s);
+          }
+          mma_commit<2>(done + 8 * buf);
+        }
+      }
+    } else if (warp >= W::kConvert0) {
+      constexpr int kRows = kTok / W::kConvert;  // tokens of one warp
+      const uint32_t ready0 = map_shared(ready, 0);
+      const int row = (warp - W::kConvert0) * kRows + (lane >> 3), chunk = lane & 7;
+      // 16-byte pieces 2c and 2c + 1 of a 128-byte row, swizzled by the row; the upper 64
+      // features write theirs in the other order, so that the eight threads of a row
+      // hit different banks
+      const int half = chunk >> 2, c = (chunk & 3) * 2;
+      int64_t ix = 0;
+      for (int w = pair; w < all && ok; w += pairs) {
+        const int tile = w % tiles, part = w / tiles;
+        const int f0 = (tile % g.feature_tiles) * 256 + rank * 128;
+        const uint32_t block = ((f0 / 32) & 15) + (chunk >> 1);
+        const int count = min(g.pieces, (part + 1) * g.per) - part * g.per;
+        for (int i = 0; i < count; ++i, ++ix) {
+          const int s = static_cast<int>(ix % kXStages);
+          ok = __all_sync(0xffffffffu, mbar_wait_bounded(ints + 8 * s, (ix / kXStages) & 1, kWaitLimit));
+          if (!ok) break;
+          const uint32_t to = xs + s * kXStage, from = to + kOperand;
+#pragma unroll
+          for (int r = 0; r < kRows; r += 4) {
+            const int t = row + r;
+            const uint4 x = ld_shared16(from + t * 128 + chunk * 16);
+            const uint32_t b = ld_shared1(from + kInts + t * 16 + block);
+            const uint32_t bits = (b == kScaleNaN ? 0x7FFFu : b << 7) * 0x10001u;
+            const __nv_bfloat162 sc = *reinterpret_cast<const __nv_bfloat162*>(&bits);
+            const uint4 v0 = make_uint4(two_values(x.x, 0x4140, sc), two_values(x.x, 0x4342, sc),
+                                        two_values(x.y, 0x4140, sc), two_values(x.y, 0x4342, sc));
+            const uint4 v1 = make_uint4(two_values(x.z, 0x4140, sc), two_values(x.z, 0x4342, sc),
+                                        two_values(x.w, 0x4140, sc), two_values(x.w, 0x4342, sc));
+            const uint32_t line = to + half * kHalf + t * 128;
+            st_shared16(line + (((c + half) ^ (t & 7)) << 4), half ? v1 : v0);
+            st_shared16(line + (((c + 1 - half) ^ (t & 7)) << 4), half ? v0 : v1);
+          }
+          fence_proxy_async_shared();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_cluster(ready0 + 8 * s);
+        }
+      }
+    }
+  } else {
+    if constexpr (kExact) asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
+    constexpr int kCols = kExact ? 128 : 256;  // columns of this warp
+    const int col0 = kExact ? (warp >> 2) * 128 : 0;
+    const uint32_t lanes = acc + (static_cast<uint32_t>(warp & 3) << 21) + col0;
+    const uint32_t freed0 = map_shared(freed, 0);
+    int n = 0;
+    for (int w = pair; w < all && ok; w += pairs) {
+      const int tile = w % tiles, part = w / tiles;
+      const int64_t feature = static_cast<int64_t>(tile % g.feature_tiles) * 256 + rank * 128 + (warp & 3) * 32 + lane;
+      const int64_t o0 = static_cast<int64_t>(tile / g.feature_tiles) * 256 + col0;
+      const int rows = static_cast<int>(min(static_cast<int64_t>(kCols), g.o - o0));  // may be 0 or less
+      auto* out = static_cast<typename Elem<kOut>::T*>(g.out) + (part * g.o + o0) * g.ld + feature;
+      const int count = min(g.pieces, (part + 1) * g.per) - part * g.per;
+      if constexpr (kExact) {
+        float sum[kCols];
+#pragma unroll
+        for (int j = 0; j < kCols; ++j) sum[j] = 0.0f;
+        for (int i = 0; i < count; i += g.chunk, ++n) {
+          const int buf = n & 1;
+          ok = __all_sync(0xffffffffu, mbar_wait_bounded(done + 8 * buf, (n >> 1) & 1, kWaitLimit));
+          if (!ok) break;
+          tcgen05_after_sync();
+#pragma unroll
+          for (int j0 = 0; j0 < kCols; j0 += 16) {
+            uint32_t v[16];
+            tmem_ld16(lanes + buf * 256 + j0, v);
+            tcgen05_wait_ld();
+#pragma unroll
+            for (int j = 0; j < 16; ++j) sum[j0 + j] += __uint_as_float(v[j]);
+          }
+          tcgen05_before_sync();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_cluster(freed0 + 8 * buf);
+        }
+        if (ok && feature < g.k) {
+#pragma unroll
+          for (int j = 0; j < kCols; ++j)
+            if (j < rows) out[j * g.ld] = Elem<kOut>::put(sum[j]);
+        }
+      } else {
+        const int buf = n & 1;
+        ++n;
+        ok = __all_sync(0xffffffffu, mbar_wait_bounded(done + 8 * buf, ((n - 1) >> 1) & 1, kWaitLimit));
+        if (!ok) break;
+        tcgen05_after_sync();
+        for (int j0 = 0; j0 < rows; j0 += 32) {
+          uint32_t v[32];
+          tmem_ld32(lanes + buf * 256 + j0, v);
+          tcgen05_wait_ld();
+          if (feature < g.k) {
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+              if (j0 + j < rows) out[(j0 + j) * g.ld] = Elem<kOut>::put(__uint_as_float(v[j]));
+          }
+        }
+        tcgen05_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster(freed0 + 8 * buf);
+      }
+    }
+  }
+  if (!ok) g_stalled_checkpoint8 = 1;
+  __syncwarp();
+  tcgen05_before_sync();
+  cluster_sync_all();  // neither CTA leaves while the other's MMAs or copies use its memory
+  if (warp == W::kLoad) {
+    tcgen05_after_sync();
+    tmem_free<2>(acc, 512);
+  }
+}
+
+// dY [t][o] as bf16 terms [kTerms][t][ld], whose sum is dY exactly: each term is the rest
+// so far cut (not rounded: no overflow) to its upper 8 bits; the largest term is the
+// last one. What is not finite is the last term, with zeros before it.
+template <int kIn, int kTerms>
+__global__ void __launch_bounds__(256)
+    k_terms(const typename Elem<kIn>::T* __restrict__ dY, int64_t ldy, bool wide, int64_t t, int64_t o,
+            __nv_bfloat16* __restrict__ out, int64_t ld) {
+  const int64_t r = static_cast<int64_t>(blockIdx.x) * blockDim.y + threadIdx.y;
+  const int64_t c = static_cast<int64_t>(blockIdx.y) * blockDim.x + threadIdx.x;
+  if (r >= t || c * 8 >= o) return;
+  float v[8];
+  load8<kIn>(dY + r * ldy, c * 8, o, wide, v);
+#pragma unroll
+  for (int term = 0; term < kTerms; ++term) {
+    uint32_t w[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      uint32_t bits = __float_as_uint(v[e]);
+      const bool finite = (bits & 0x7f800000u) != 0x7f800000u;
+      if (!finite && (bits & 0x7fffffu)) bits |= 0x400000u;  // a NaN stays one
+      w[e] = bits >> 16;
+      v[e] = finite ? v[e] - __uint_as_float(bits & 0xffff0000u) : 0.0f;
+    }
+    *reinterpret_cast<uint4*>(out + ((kTerms - 1 - term) * t + r) * ld + c * 8) =
+        make_uint4(w[0] | w[1] << 16, w[2] | w[3] << 16, w[4] | w[5] << 16, w[6] | w[7] << 16);
+  }
+}
+
+// dW = the sum of `split` partial matrices [o][k], in their order.
+template <int kOut>
+__global__ void __launch_bounds__(256)
+    k_join(const float* __restrict__ part, int split, int64_t o, int64_t k, typename Elem<kOut>::T* __restrict__ dW,
+           int64_t ldw) {
+  const int64_t c = static_cast<int64_t>(blockIdx.y) * 256 + threadIdx.x, r = blockIdx.x;
+  if (c >= k) return;
+  float sum = 0.0f;
+  for (int i = 0; i < split; ++i) sum += part[(i * o + r) * k + c];
+  dW[r * ldw + c] = Elem<kOut>::put(sum);
+}
+
+template <int kOut>
+__global__ void __launch_bounds__(256)
+    k_zero(int64_t k, typename Elem<kOut>::T* __restrict__ dW, int64_t ldw) {
+  const int64_t c = static_cast<int64_t>(blockIdx.y) * 256 + threadIdx.x;
+  if (c < k) dW[static_cast<int64_t>(blockIdx.x) * ldw + c] = Elem<kOut>::put(0.0f);
+}
+
+// How a gradient is cut: bf16 terms and whether dY is copied into them, parts of the
+// token axis, and the workspace.
+struct GradientPlan {
+  int terms, split, per;
+  bool copy;
+  int64_t ld;  // pitch of the copied terms
+  size_t terms_bytes, bytes;
+};
+GradientPlan gradient_plan(const void* dY, int64_t t, int64_t o, int64_t k, int type, int64_t ldy) {
+  GradientPlan p = {};
+  p.terms = type == kF32 ? 3 : (type == kF16 ? 2 : 1);
+  // TMA reads bf16 rows in place when they start on 16-byte boundaries
+  p.copy = type != kBF16 || (t > 1 && ldy % 8 != 0) || (reinterpret_cast<uintptr_t>(dY) & 15) != 0;
+  p.ld = (o + 7) / 8 * 8;
+  const int64_t pieces = (t + kTok - 1) / kTok, tiles = ((o + 255) / 256) * ((k + 255) / 256);
+  const int64_t pairs = sm_count() / 2;
+  int64_t split = tiles < pairs ? pairs / tiles : 1;
+  split = std::max<int64_t>(1, std::min(split, pieces / 8));
+  p.per = static_cast<int>((pieces + split - 1) / split);
+  p.split = static_cast<int>((pieces + p.per - 1) / p.per);
+  p.terms_bytes = p.copy ? (static_cast<size_t>(p.terms) * t * p.ld * 2 + 255) / 256 * 256 : 0;
+  p.bytes = p.terms_bytes + (p.split > 1 ? static_cast<size_t>(p.split) * o * k * 4 : 0);
+  return p;
+}
+
+template <int kIn, int kTerms>
+void split_terms(const void* dY, int64_t ldy, int64_t t, int64_t o, __nv_bfloat16* out, int64_t ld, cudaStream_t st) {
+  dim3 grid, block;
+  piece_grid(t, (o + 7) / 8, &grid, &block);
+  k_terms<kIn, kTerms><<<grid, block, 0, st>>>(static_cast<const typename Elem<kIn>::T*>(dY), ldy,
+                                               rows_aligned16(dY, ldy, type_bytes(kIn)), t, o, out, ld);
+  note_launch();
+}
+
+template <int kOut, bool kExact>
+cudaError_t wgrad(const CUtensorMap& map_q, const CUtensorMap& map_s, const CUtensorMap& map_y, const Gradient& g,
+                  cudaStream_t st) {
+  const cudaError_t e = cudaFuncSetAttribute(k_wgrad<kOut, kExact>, cudaFuncAttributeMaxDynamicSharedMemorySize, kGradSmem);
+  if (e != cudaSuccess) return e;
+  const int64_t all = static_cast<int64_t>(g.feature_tiles) * g.output_tiles * g.split;
+  const int pairs = static_cast<int>(std::min<int64_t>(sm_count() / 2, all));
+  k_wgrad<kOut, kExact><<<2 * pairs, GradWarps<kExact>::kThreads, kGradSmem, st>>>(map_q, map_s, map_y, g);
+  note_launch();
+  return cudaGetLastError();
+}
+
+template <int kOut>
+cudaError_t wgrad_all(const CUtensorMap& map_q, const CUtensorMap& map_s, const CUtensorMap& map_y, Gradient g,
+                      float* part, void* dW, int64_t ldw, cudaStream_t st) {
+  constexpr bool kExact = kOut != kBF16;
+  // 16 steps of 16 tokens per accumulator, where the terms after the first piece's smaller ones count as steps too
+  g.chunk = !kExact ? g.per : (g.terms == 1 ? 4 : 2);
+  if (g.split == 1) {
+    g.out = dW;
+    g.ld = ldw;
+    return wgrad<kOut, kExact>(map_q, map_s, map_y, g, st);
+  }
+  g.out = part;
+  g.ld = g.k;
+  const cudaError_t e = wgrad<kF32, kExact>(map_q, map_s, map_y, g, st);
+  if (e != cudaSuccess) return e;
+  k_join<kOut><<<dim3(static_cast<unsigned>(g.o), static_cast<unsigned>((g.k + 255) / 256)), 256, 0, st>>>(
+      part, g.split, g.o, g.k, static_cast<typename Elem<kOut>::T*>(dW), ldw);
   note_launch();
   return cudaGetLastError();
 }
@@ -186,14 +558,75 @@ cudaError_t launch_checkpoint8_restore(const int8_t* q, int64_t ldq, const uint8
   return cudaGetLastError();
 }
 
-size_t checkpoint8_wgrad_workspace(int64_t, int64_t, int64_t, int, int64_t) { return 0; }
+size_t checkpoint8_wgrad_workspace(const void* dY, int dy_type, int64_t ldy, int64_t t, int64_t o, int64_t k) {
+  return t == 0 ? 0 : gradient_plan(dY, t, o, k, dy_type, ldy).bytes;
+}
 
 cudaError_t launch_checkpoint8_wgrad(const void* dY, int dy_type, int64_t ldy, const int8_t* q, int64_t ldq,
                                      const uint8_t* scale, int64_t lds, int64_t t, int64_t o, int64_t k, void* dW,
-                                     int dw_type, int64_t ldw, void*, cudaStream_t st) {
-  if (dy_type == kF32) return wgrad_plain<kF32>(dY, ldy, q, ldq, scale, lds, t, o, k, dW, dw_type, ldw, st);
-  if (dy_type == kBF16) return wgrad_plain<kBF16>(dY, ldy, q, ldq, scale, lds, t, o, k, dW, dw_type, ldw, st);
-  return wgrad_plain<kF16>(dY, ldy, q, ldq, scale, lds, t, o, k, dW, dw_type, ldw, st);
+                                     int dw_type, int64_t ldw, void* ws, cudaStream_t st) {
+  if (t == 0) {
+    const dim3 grid(static_cast<unsigned>(o), static_cast<unsigned>((k + 255) / 256));
+    if (dw_type == kF32)
+      k_zero<kF32><<<grid, 256, 0, st>>>(k, static_cast<float*>(dW), ldw);
+    else if (dw_type == kBF16)
+      k_zero<kBF16><<<grid, 256, 0, st>>>(k, static_cast<__nv_bfloat16*>(dW), ldw);
+    else
+      k_zero<kF16><<<grid, 256, 0, st>>>(k, static_cast<__half*>(dW), ldw);
+    note_launch();
+    return cudaGetLastError();
+  }
+  const GradientPlan p = gradient_plan(dY, t, o, k, dy_type, ldy);
+  auto* terms = static_cast<__nv_bfloat16*>(ws);
+  if (p.copy) {
+    if (dy_type == kF32)
+      split_terms<kF32, 3>(dY, ldy, t, o, terms, p.ld, st);
+    else if (dy_type == kF16)
+      split_terms<kF16, 2>(dY, ldy, t, o, terms, p.ld, st);
+    else
+      split_terms<kBF16, 1>(dY, ldy, t, o, terms, p.ld, st);
+    dY = terms;
+    ldy = p.ld;
+  }
+  if (t == 1) ldy = (o + 7) / 8 * 8;  // one row: its pitch is never used
+  CUtensorMap map_q, map_s, map_y;
+  const uint64_t rows = static_cast<uint64_t>(t);
+  const uint64_t sizes_q[2] = {static_cast<uint64_t>(k), rows}, strides_q[1] = {static_cast<uint64_t>(ldq)};
+  const uint64_t sizes_s[2] = {static_cast<uint64_t>((k + 31) / 32), rows}, strides_s[1] = {static_cast<uint64_t>(lds)};
+  const uint64_t sizes_y[3] = {static_cast<uint64_t>(o), rows, static_cast<uint64_t>(p.terms)};
+  const uint64_t strides_y[2] = {static_cast<uint64_t>(ldy) * 2, static_cast<uint64_t>(ldy) * 2 * rows};
+  const uint32_t box_q[2] = {128, kTok}, box_s[2] = {16, kTok}, box_y[3] = {64, kTok, 1};
+  if (!make_map(&map_q, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, q, sizes_q, strides_q, box_q, CU_TENSOR_MAP_SWIZZLE_NONE) ||
+      !make_map(&map_s, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, scale, sizes_s, strides_s, box_s, CU_TENSOR_MAP_SWIZZLE_NONE) ||
+      !make_map(&map_y, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, dY, sizes_y, strides_y, box_y, CU_TENSOR_MAP_SWIZZLE_128B))
+    return cudaErrorInvalidValue;
+  Gradient g = {};
+  g.o = o;
+  g.k = k;
+  g.feature_tiles = static_cast<int>((k + 255) / 256);
+  g.output_tiles = static_cast<int>((o + 255) / 256);
+  g.pieces = static_cast<int>((t + kTok - 1) / kTok);
+  g.terms = p.terms;
+  g.split = p.split;
+  g.per = p.per;
+  if (static_cast<int64_t>(g.feature_tiles) * g.output_tiles > INT32_MAX / 256) return cudaErrorInvalidValue;
+  auto* part = reinterpret_cast<float*>(static_cast<unsigned char*>(ws) + p.terms_bytes);
+  switch (dw_type) {
+    case kF32: return wgrad_all<kF32>(map_q, map_s, map_y, g, part, dW, ldw, st);
+    case kBF16: return wgrad_all<kBF16>(map_q, map_s, map_y, g, part, dW, ldw, st);
+    default: return wgrad_all<kF16>(map_q, map_s, map_y, g, part, dW, ldw, st);
+  }
+}
+
+cudaError_t checkpoint8_stalled(bool* stalled) {
+  int v = 0;
+  cudaError_t e = cudaMemcpyFromSymbol(&v, g_stalled_checkpoint8, sizeof(v));
+  *stalled = v != 0;
+  if (e == cudaSuccess && v) {
+    v = 0;
+    e = cudaMemcpyToSymbol(g_stalled_checkpoint8, &v, sizeof(v));
+  }
+  return e;
 }
 
 }  // namespace ecasq

@@ -198,9 +198,10 @@ cudaError_t launch_checkpoint8(const void* X, int type, int64_t t, int64_t k, in
                                cudaStream_t st);
 cudaError_t launch_checkpoint8_restore(const int8_t* q, int64_t ldq, const uint8_t* scale, int64_t lds, int64_t t,
                                        int64_t k, void* X, int type, int64_t ldx, cudaStream_t st);
-size_t checkpoint8_wgrad_workspace(int64_t t, int64_t o, int64_t k, int dy_type, int64_t ldy);
+size_t checkpoint8_wgrad_workspace(const void* dY, int dy_type, int64_t ldy, int64_t t, int64_t o, int64_t k);
 cudaError_t launch_checkpoint8_wgrad(const void* dY, int dy_type, int64_t ldy, const int8_t* q, int64_t ldq,
                                      const uint8_t* scale, int64_t lds, int64_t t, int64_t o, int64_t k, void* dW,
                                      int dw_type, int64_t ldw, void* ws, cudaStream_t st);
+cudaError_t checkpoint8_stalled(bool* stalled);  // waits for the device; clears the mark
 
 }  // namespace ecasq

@@ -81,7 +81,7 @@ def load(path: str = LIB_PATH):
         "ecasq_int8_matmul": (I, [P, I64, P, P, I64, P, P, I64, I64, I64, P, I, I64, P]),
         "ecasq_checkpoint8": (I, [P, I, I64, I64, I64, U64, P, P, I64, P, I64, P]),
         "ecasq_checkpoint8_restore": (I, [P, I64, P, I64, I64, I64, P, I, I64, P]),
-        "ecasq_checkpoint8_wgrad_workspace_size": (SZ, [I64, I64, I64, I, I64]),
+        "ecasq_checkpoint8_wgrad_workspace_size": (SZ, [P, I, I64, I64, I64, I64]),
         "ecasq_checkpoint8_wgrad": (I, [P, I, I64, P, I64, P, I64, I64, I64, I64, P, I, I64, P, SZ, P]),
         "ecasq_device_stalled": (I, []),
     }
@@ -617,7 +617,7 @@ def checkpoint8_wgrad(dY: torch.Tensor, q: torch.Tensor, scale: torch.Tensor, ou
         raise EcasqError(f"out_dtype must be float32, bfloat16 or float16, not {out_dtype}")
     dW = torch.empty((o, k), dtype=out_dtype, device=dev)
     ty = _TYPES[dY.dtype]
-    need = L.ecasq_checkpoint8_wgrad_workspace_size(t, o, k, ty, ldy)
+    need = L.ecasq_checkpoint8_wgrad_workspace_size(dY.data_ptr(), ty, ldy, t, o, k)
     # the caching allocator's, so that it belongs to this call (or to the graph that captures it) alone
     ws = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
     _call("ecasq_checkpoint8_wgrad", dev, dY.data_ptr(), ty, ldy, q.data_ptr(), ldq, scale.data_ptr(), lds, t, o, k,

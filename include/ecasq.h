@@ -386,9 +386,11 @@ int ecasq_checkpoint8_restore(const int8_t* q, int64_t ldq, const uint8_t* scale
  * bfloat16 terms whose sum it is), sums are float32, the result is rounded once
  * to dw_type. Long sums over few output entries are split over the tokens and
  * joined in a fixed order, so results repeat. Workspace:
- * ecasq_checkpoint8_wgrad_workspace_size for the same sizes, types and pitch on
- * the current device; it may be 0. */
-size_t ecasq_checkpoint8_wgrad_workspace_size(int64_t t, int64_t o, int64_t k, int dy_type, int64_t ldy);
+ * ecasq_checkpoint8_wgrad_workspace_size for the same dY (its address is not
+ * read through, only its alignment counts), sizes and pitch on the current
+ * device; it may be 0. */
+size_t ecasq_checkpoint8_wgrad_workspace_size(const void* dY, int dy_type, int64_t ldy, int64_t t, int64_t o,
+                                              int64_t k);
 int ecasq_checkpoint8_wgrad(const void* dY, int dy_type, int64_t ldy, const int8_t* q, int64_t ldq,
                             const uint8_t* scale, int64_t lds, int64_t t, int64_t o, int64_t k, void* dW, int dw_type,
                             int64_t ldw, void* ws, size_t ws_bytes, void* stream);

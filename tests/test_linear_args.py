@@ -64,7 +64,7 @@ def test_gradient_arguments(lib):
         args[at] = bad
         assert f(*args) == -1, (at, bad)
     size = lib.ecasq_checkpoint8_wgrad_workspace_size
-    assert size(-1, 64, 100, 1, 64) == 0 and size(4, 0, 100, 1, 64) == 0 and size(4, 64, 100, 9, 64) == 0
+    assert size(P16, 1, 64, -1, 64, 100) == 0 and size(P16, 1, 64, 4, 0, 100) == 0 and size(P16, 9, 64, 4, 64, 100) == 0
 
 
 def test_no_cpu_path():
