@@ -517,6 +517,23 @@ int ecasq_int8_matmul(const int8_t* A, int64_t lda, const float* sa, const int8_
                                         static_cast<cudaStream_t>(stream)));
 }
 
+size_t ecasq_int8_linear_workspace_size(int64_t m, int64_t k) {
+  return valid_rows(m, k) && k <= kMaxK8 ? int8_linear_workspace(m, k) : 0;
+}
+
+int ecasq_int8_linear(const void* X, int x_type, int64_t ldx, const int8_t* B, int64_t ldb, const float* sb,
+                      const float* bias, int64_t m, int64_t n, int64_t k, void* Y, int64_t ldy, void* ws,
+                      size_t ws_bytes, void* stream) {
+  if (!valid_type(x_type) || !valid_rows(m, k) || n < 1 || n > kMaxRows8 || k > kMaxK8) return ECASQ_ERR_ARG;
+  if (m == 0) return ECASQ_OK;
+  if (!X || !valid_pitch(m, k, ldx) || !valid_bytes(B, k, ldb, 16) || !sb || !Y || !valid_pitch(m, n, ldy))
+    return ECASQ_ERR_ARG;
+  const size_t need = int8_linear_workspace(m, k);
+  if (need && (!ws || ws_bytes < need || (reinterpret_cast<uintptr_t>(ws) & 15) != 0)) return ECASQ_ERR_WORKSPACE;
+  return cuda_status(
+      launch_int8_linear(X, x_type, ldx, B, ldb, sb, bias, m, n, k, Y, ldy, ws, static_cast<cudaStream_t>(stream)));
+}
+
 int ecasq_checkpoint8(const void* X, int x_type, int64_t t, int64_t k, int64_t ldx, uint64_t seed,
                       const uint64_t* seed_add, int8_t* q, int64_t ldq, uint8_t* scale, int64_t lds, void* stream) {
   if (!valid_type(x_type) || !valid_rows(t, k)) return ECASQ_ERR_ARG;

@@ -32,6 +32,33 @@ __device__ __forceinline__ int nearest127(float x, float xs, float r, float a) {
   return q;
 }
 
+// A row's quantisation from its largest magnitude, given as bits (NaN and infinity
+// order above every finite value).
+struct RowScale {
+  float a, lift, inv, scale;
+  bool bad;
+};
+__device__ __forceinline__ RowScale row_scale(uint32_t a_bits) {
+  RowScale s;
+  s.bad = a_bits >= 0x7f800000u;
+  s.a = __uint_as_float(a_bits);
+  // tiny rows are lifted by 2^80 (exact) so that 127 / a stays finite
+  s.lift = s.a < 0x1p-60f ? 0x1p80f : 1.0f;
+  s.inv = (s.bad || a_bits == 0) ? 0.0f : __fdiv_rn(127.0f, s.a * s.lift);
+  s.scale = s.bad ? __uint_as_float(0x7fc00000u) : __fdiv_rn(s.a, 127.0f);
+  return s;
+}
+// Eight integers of a row, in order.
+__device__ __forceinline__ uint2 quantize8(const float (&v)[8], const RowScale& s) {
+  uint32_t word[2] = {0, 0};
+  if (s.inv != 0.0f) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      word[e >> 2] |= (static_cast<uint32_t>(nearest127(v[e], v[e] * s.lift, s.inv, s.a)) & 0xffu) << (8 * (e & 3));
+  }
+  return make_uint2(word[0], word[1]);
+}
+
 template <int kType, int kTPR, int kKeep, bool kLong>
 __global__ void __launch_bounds__(kTPR < 128 ? 128 : kTPR)
     k_int8_rows(const typename Elem<kType>::T* __restrict__ X, int64_t n, int64_t k, int64_t ldx, bool wide,
@@ -67,28 +94,19 @@ __global__ void __launch_bounds__(kTPR < 128 ? 128 : kTPR)
     m = __reduce_max_sync(0xffffffffu, m);
   }
   if (!live) return;
-  const bool bad = m >= 0x7f800000u;
-  const float a = __uint_as_float(m);
-  // tiny rows are lifted by 2^80 (exact) so that 127 / a stays finite
-  const float lift = a < 0x1p-60f ? 0x1p80f : 1.0f;
-  const float inv = (bad || m == 0) ? 0.0f : __fdiv_rn(127.0f, a * lift);
+  const RowScale a = row_scale(m);
   if (lane == 0) {
-    scale[r] = bad ? __uint_as_float(0x7fc00000u) : __fdiv_rn(a, 127.0f);
-    status[r] = bad ? kStatusRange : kStatusOk;
+    scale[r] = a.scale;
+    status[r] = a.bad ? kStatusRange : kStatusOk;
   }
   int8_t* out = Q + r * ldq;
   const auto put = [&](int64_t j, const float(&w)[8]) {
     if (j >= k) return;
-    uint32_t word[2] = {0, 0};
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const int q = bad || m == 0 ? 0 : nearest127(w[e], w[e] * lift, inv, a);
-      word[e >> 2] |= (static_cast<uint32_t>(q) & 0xffu) << (8 * (e & 3));
-    }
+    const uint2 q = quantize8(w, a);
     if (j + 8 <= k) {
-      *reinterpret_cast<uint2*>(out + j) = make_uint2(word[0], word[1]);
+      *reinterpret_cast<uint2*>(out + j) = q;
     } else {
-      for (int e = 0; j + e < k; ++e) out[j + e] = static_cast<int8_t>(word[e >> 2] >> (8 * (e & 3)));
+      for (int e = 0; j + e < k; ++e) out[j + e] = static_cast<int8_t>((e < 4 ? q.x : q.y) >> (8 * (e & 3)));
     }
   };
 #pragma unroll
@@ -474,6 +492,152 @@ cudaError_t int8_pair(const CUtensorMap& map_w, const CUtensorMap& map_x, const 
   return cudaGetLastError();
 }
 
+// -- up to 8 tokens: the weights' bytes are the cost, and one launch. Each CTA holds
+// all tokens in shared memory (quantising them itself when they come as floats) and
+// its warps take output channels in turn, a lane 16 bytes of k at a time (dp4a). The
+// first channels' weights are on their way while the tokens are quantised. --
+
+constexpr int kFewTokens = 8;
+constexpr int64_t kFewBytes = 64 << 10;  // shared memory of the tokens
+constexpr int kFewThreads = 256;
+
+// 16 bytes of a row of weights, zeros beyond k.
+__device__ __forceinline__ int4 weights16(const int8_t* __restrict__ row, int64_t at, int64_t k) {
+  if (at + 16 <= k) return __ldg(reinterpret_cast<const int4*>(row + at));
+  int4 v = make_int4(0, 0, 0, 0);
+  int* w = reinterpret_cast<int*>(&v);
+#pragma unroll
+  for (int e = 0; e < 16; ++e)
+    if (at + e < k) w[e >> 2] |= (row[at + e] & 0xff) << (8 * (e & 3));
+  return v;
+}
+
+// kIn: the tokens' type, or -1 for rows that are quantised already (A, sa).
+template <int kIn, int kType, int kM>
+__global__ void __launch_bounds__(kFewThreads)
+    k_int8_few(const void* __restrict__ X, int64_t ldx, bool wide, const int8_t* __restrict__ B, int64_t ldb,
+               const Product p, int64_t k) {
+  extern __shared__ int4 tokens[];  // [m][kp / 16]
+  __shared__ uint32_t part[kFewThreads / 32][kM];
+  __shared__ float token_scale[kM];
+  constexpr int kRows = kM >= 4 ? 2 : 1;  // channels of a warp at a time
+  constexpr int kAhead = kM >= 4 ? 4 : 8;  // pieces of 16 bytes of each in flight per lane
+  const int warp = warp_id(), lane = lane_id();
+  const int kp = static_cast<int>((k + 15) / 16);
+  const int m = static_cast<int>(p.m);
+  const int64_t step = static_cast<int64_t>(gridDim.x) * (kFewThreads / 32) * kRows;
+  int64_t channel = (static_cast<int64_t>(blockIdx.x) * (kFewThreads / 32) + warp) * kRows;
+  int4 w[kRows][kAhead];
+  const auto load = [&](int64_t c0, int at) {
+#pragma unroll
+    for (int r = 0; r < kRows; ++r)
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) {
+        const int piece = at + lane + 32 * i;
+        w[r][i] = make_int4(0, 0, 0, 0);
+        if (piece < kp && c0 + r < p.n) w[r][i] = weights16(B + (c0 + r) * ldb, static_cast<int64_t>(piece) * 16, k);
+      }
+  };
+  load(channel, 0);
+
+  if constexpr (kIn >= 0) {
+    using T = typename Elem<kIn < 0 ? 0 : kIn>::T;
+    const T* x = static_cast<const T*>(X);
+    uint32_t top[kM];
+#pragma unroll
+    for (int j = 0; j < kM; ++j) {
+      top[j] = 0;
+      if (j < m)
+        for (int64_t c = threadIdx.x * 8; c < k; c += kFewThreads * 8) {
+          float v[8];
+          load8<kIn < 0 ? 0 : kIn>(x + j * ldx, c, k, wide, v);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) top[j] = max(top[j], __float_as_uint(v[e]) & 0x7fffffffu);
+        }
+      top[j] = __reduce_max_sync(0xffffffffu, top[j]);
+      if (lane == 0) part[warp][j] = top[j];
+    }
+    __syncthreads();
+#pragma unroll
+    for (int j = 0; j < kM; ++j) {
+      if (j >= m) break;
+      const uint32_t a_bits = __reduce_max_sync(0xffffffffu, part[lane % (kFewThreads / 32)][j]);
+      const RowScale a = row_scale(a_bits);
+      if (threadIdx.x == 0) token_scale[j] = a.scale;
+      for (int64_t c = threadIdx.x * 8; c < static_cast<int64_t>(kp) * 16; c += kFewThreads * 8) {
+        float v[8];
+        load8<kIn < 0 ? 0 : kIn>(x + j * ldx, c, k, wide, v);
+        const uint2 q = quantize8(v, a);
+        reinterpret_cast<uint2*>(tokens)[static_cast<int64_t>(j) * kp * 2 + c / 8] = q;
+      }
+    }
+  } else {
+    const int8_t* x = static_cast<const int8_t*>(X);
+    for (int j = 0; j < m; ++j)
+      for (int c = threadIdx.x; c < kp; c += kFewThreads)
+        tokens[j * kp + c] = weights16(x + j * ldx, static_cast<int64_t>(c) * 16, k);
+    if (threadIdx.x < m) token_scale[threadIdx.x] = p.sa[threadIdx.x];
+  }
+  __syncthreads();
+
+  for (; channel < p.n; channel += step) {
+    int acc[kRows][kM] = {};
+    for (int at = 0; at < kp; at += 32 * kAhead) {
+      if (at > 0) load(channel, at);
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) {
+        const int piece = at + lane + 32 * i;
+        if (piece < kp) {
+#pragma unroll
+          for (int j = 0; j < kM; ++j) {
+            if (j >= m) break;
+            const int4 x = tokens[j * kp + piece];
+#pragma unroll
+            for (int r = 0; r < kRows; ++r)
+              acc[r][j] = __dp4a(w[r][i].w, x.w, __dp4a(w[r][i].z, x.z, __dp4a(w[r][i].y, x.y, __dp4a(w[r][i].x, x.x, acc[r][j]))));
+          }
+        }
+      }
+    }
+    load(channel + step, 0);
+#pragma unroll
+    for (int r = 0; r < kRows; ++r) {
+      int mine = 0;
+#pragma unroll
+      for (int j = 0; j < kM; ++j) {
+        const int sum = __reduce_add_sync(0xffffffffu, acc[r][j]);
+        if (lane == j) mine = sum;
+      }
+      const int64_t c = channel + r;
+      if (lane < m && c < p.n)
+        put_output<kType>(p, lane, c, mine, token_scale[lane], p.sb[c], p.bias ? p.bias[c] : 0.0f);
+    }
+  }
+}
+
+template <int kIn, int kType>
+cudaError_t int8_few_tokens(const void* X, int64_t ldx, const int8_t* B, int64_t ldb, const Product& p, int64_t k,
+                            cudaStream_t st) {
+  const size_t smem = static_cast<size_t>(p.m) * ((k + 15) / 16 * 16);
+  const bool wide = kIn >= 0 && rows_aligned16(X, ldx, type_bytes(kIn));
+  const auto run = [&](auto kernel, int rows) {
+    if (smem > 48 << 10) {
+      const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kFewBytes));
+      if (e != cudaSuccess) return e;
+    }
+    const int64_t per = kFewThreads / 32 * rows, most = static_cast<int64_t>(sm_count()) * 4;
+    kernel<<<static_cast<unsigned>(std::min((p.n + per - 1) / per, most)), kFewThreads, smem, st>>>(X, ldx, wide, B, ldb, p, k);
+    note_launch();
+    return cudaGetLastError();
+  };
+  if (p.m == 1) return run(k_int8_few<kIn, kType, 1>, 1);
+  if (p.m == 2) return run(k_int8_few<kIn, kType, 2>, 1);
+  if (p.m <= 4) return run(k_int8_few<kIn, kType, 4>, 2);
+  return run(k_int8_few<kIn, kType, 8>, 2);
+}
+
+bool few_tokens(int64_t m, int64_t k) { return m <= kFewTokens && m * ((k + 15) / 16 * 16) <= kFewBytes; }
+
 // A map of 8-bit rows in boxes of 128 bytes by `rows`.
 bool map_rows8(CUtensorMap* map, const int8_t* p, int64_t n, int64_t k, int64_t ld, int rows) {
   const uint64_t sizes[2] = {static_cast<uint64_t>(k), static_cast<uint64_t>(n)}, strides[1] = {static_cast<uint64_t>(ld)};
@@ -482,8 +646,8 @@ bool map_rows8(CUtensorMap* map, const int8_t* p, int64_t n, int64_t k, int64_t 
 }
 
 template <int kType, int kTok>
-cudaError_t int8_few(const int8_t* A, int64_t lda, const int8_t* B, int64_t ldb, const Product& p, int64_t k,
-                     cudaStream_t st) {
+cudaError_t int8_split(const int8_t* A, int64_t lda, const int8_t* B, int64_t ldb, const Product& p, int64_t k,
+                       cudaStream_t st) {
   CUtensorMap map_w, map_x;
   if (!map_rows8(&map_w, B, p.n, k, ldb, 128) || !map_rows8(&map_x, A, p.m, k, lda, kTok)) return cudaErrorInvalidValue;
   const int64_t tiles = (p.n + 127) / 128 * ((p.m + kTok - 1) / kTok);
@@ -498,10 +662,11 @@ cudaError_t int8_few(const int8_t* A, int64_t lda, const int8_t* B, int64_t ldb,
 template <int kType>
 cudaError_t int8_product(const int8_t* A, int64_t lda, const int8_t* B, int64_t ldb, const Product& p, int64_t k,
                          cudaStream_t st) {
-  if (p.m <= 16) return int8_few<kType, 16>(A, lda, B, ldb, p, k, st);
-  if (p.m <= 32) return int8_few<kType, 32>(A, lda, B, ldb, p, k, st);
-  if (p.m <= 64) return int8_few<kType, 64>(A, lda, B, ldb, p, k, st);
-  if (p.m <= 256) return int8_few<kType, 128>(A, lda, B, ldb, p, k, st);
+  if (few_tokens(p.m, k)) return int8_few_tokens<-1, kType>(A, lda, B, ldb, p, k, st);
+  if (p.m <= 16) return int8_split<kType, 16>(A, lda, B, ldb, p, k, st);
+  if (p.m <= 32) return int8_split<kType, 32>(A, lda, B, ldb, p, k, st);
+  if (p.m <= 64) return int8_split<kType, 64>(A, lda, B, ldb, p, k, st);
+  if (p.m <= 256) return int8_split<kType, 128>(A, lda, B, ldb, p, k, st);
   CUtensorMap map_w, map_x;
   if (!map_rows8(&map_w, B, p.n, k, ldb, 128) || !map_rows8(&map_x, A, p.m, k, lda, 128)) return cudaErrorInvalidValue;
   return int8_pair<kType>(map_w, map_x, p, st);
@@ -527,6 +692,31 @@ cudaError_t launch_int8_matmul(const int8_t* A, int64_t lda, const float* sa, co
     case kBF16: return int8_product<kBF16>(A, lda, B, ldb, p, k, st);
     default: return int8_product<kF16>(A, lda, B, ldb, p, k, st);
   }
+}
+
+size_t int8_linear_workspace(int64_t m, int64_t k) {
+  if (m == 0 || few_tokens(m, k)) return 0;
+  return static_cast<size_t>(m) * ((k + 31) / 32 * 32 + 8);  // integers, scales, status
+}
+
+cudaError_t launch_int8_linear(const void* X, int x_type, int64_t ldx, const int8_t* B, int64_t ldb, const float* sb,
+                               const float* bias, int64_t m, int64_t n, int64_t k, void* Y, int64_t ldy, void* ws,
+                               cudaStream_t st) {
+  if (few_tokens(m, k)) {
+    const Product p = {nullptr, sb, bias, Y, m, n, ldy, 0};
+    switch (x_type) {
+      case kF32: return int8_few_tokens<kF32, kF32>(X, ldx, B, ldb, p, k, st);
+      case kBF16: return int8_few_tokens<kBF16, kBF16>(X, ldx, B, ldb, p, k, st);
+      default: return int8_few_tokens<kF16, kF16>(X, ldx, B, ldb, p, k, st);
+    }
+  }
+  const int64_t ldq = (k + 31) / 32 * 32;
+  auto* q = static_cast<int8_t*>(ws);
+  auto* scale = reinterpret_cast<float*>(q + m * ldq);
+  const cudaError_t e =
+      launch_int8_quantize(X, x_type, m, k, ldx, q, ldq, scale, reinterpret_cast<int32_t*>(scale + m), st);
+  if (e != cudaSuccess) return e;
+  return launch_int8_matmul(q, ldq, scale, B, ldb, sb, bias, m, n, k, Y, x_type, ldy, st);
 }
 
 cudaError_t int8_stalled(bool* stalled) {

@@ -190,6 +190,10 @@ cudaError_t launch_int8_quantize(const void* X, int type, int64_t n, int64_t k, 
 cudaError_t launch_int8_matmul(const int8_t* A, int64_t lda, const float* sa, const int8_t* B, int64_t ldb,
                                const float* sb, const float* bias, int64_t m, int64_t n, int64_t k, void* Y, int type,
                                int64_t ldy, cudaStream_t st);
+size_t int8_linear_workspace(int64_t m, int64_t k);
+cudaError_t launch_int8_linear(const void* X, int x_type, int64_t ldx, const int8_t* B, int64_t ldb, const float* sb,
+                               const float* bias, int64_t m, int64_t n, int64_t k, void* Y, int64_t ldy, void* ws,
+                               cudaStream_t st);
 cudaError_t int8_stalled(bool* stalled);  // waits for the device; clears the mark
 
 // ---- activation checkpoints in 8 bits (checkpoint8.cu) ----

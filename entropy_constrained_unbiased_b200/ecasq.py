@@ -7,6 +7,7 @@ fallback: loading raises if the library is missing or no CUDA device exists.
 from __future__ import annotations
 
 import ctypes as C
+import functools
 import os
 
 import torch
@@ -24,7 +25,8 @@ EXPORTS = [
     "ecasq_solve_approx_budget_stats",
     "ecasq_encode", "ecasq_dequantize", "ecasq_entropy", "ecasq_rans_segments", "ecasq_rans_segment_words",
     "ecasq_rans_encode", "ecasq_rans_decode", "ecasq_status_string", "ecasq_launch_count",
-    "ecasq_int8_quantize", "ecasq_int8_matmul", "ecasq_checkpoint8", "ecasq_checkpoint8_restore",
+    "ecasq_int8_quantize", "ecasq_int8_matmul", "ecasq_int8_linear_workspace_size", "ecasq_int8_linear",
+    "ecasq_checkpoint8", "ecasq_checkpoint8_restore",
     "ecasq_checkpoint8_wgrad_workspace_size", "ecasq_checkpoint8_wgrad", "ecasq_device_stalled",
 ]
 
@@ -79,6 +81,8 @@ def load(path: str = LIB_PATH):
         "ecasq_launch_count": (C.c_uint64, [I]),
         "ecasq_int8_quantize": (I, [P, I, I64, I64, I64, P, I64, P, P, P]),
         "ecasq_int8_matmul": (I, [P, I64, P, P, I64, P, P, I64, I64, I64, P, I, I64, P]),
+        "ecasq_int8_linear_workspace_size": (SZ, [I64, I64]),
+        "ecasq_int8_linear": (I, [P, I, I64, P, I64, P, P, I64, I64, I64, P, I64, P, SZ, P]),
         "ecasq_checkpoint8": (I, [P, I, I64, I64, I64, U64, P, P, I64, P, I64, P]),
         "ecasq_checkpoint8_restore": (I, [P, I64, P, I64, I64, I64, P, I, I64, P]),
         "ecasq_checkpoint8_wgrad_workspace_size": (SZ, [P, I, I64, I64, I64, I64]),
@@ -468,28 +472,39 @@ def rans_decode(words: torch.Tensor, seg_len: torch.Tensor, hist: torch.Tensor, 
 
 
 # -- 8-bit operators: integer linear layer, activation checkpoints ----------------------
+#
+# These calls run on the current stream of their tensors' device, whichever device is
+# current, and their workspaces are the caching allocator's, so that each belongs to
+# its call (or to the graph that captures it) alone. A call of a few microseconds is
+# bound by this code: it looks at each tensor once.
 
 _TYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
+_stream_of = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
-def _matrix(t, name, dtypes, device=None):
-    """Checks a [rows, cols] CUDA matrix with adjacent columns; returns (rows, cols, row pitch)."""
-    if not t.is_cuda or t.dtype not in dtypes or t.dim() != 2:
+def _matrix(t, name, dtypes, index=None):
+    """Checks a [rows, cols] CUDA matrix with adjacent columns (on device `index`);
+    returns (rows, cols, row pitch)."""
+    at = t.get_device()
+    if at < 0 or t.dtype not in dtypes or t.dim() != 2:
         raise EcasqError(f"{name} must be a 2-D CUDA tensor of {' or '.join(str(d) for d in dtypes)}")
-    if device is not None and t.device != device:
-        raise EcasqError(f"{name} is on {t.device}, not {device}")
+    if index is not None and at != index:
+        raise EcasqError(f"{name} is on cuda:{at}, not cuda:{index}")
     n, k = t.shape
-    if k < 1 or (k > 1 and t.stride(1) != 1):
+    ld, one = t.stride()
+    if k < 1 or (k > 1 and one != 1):
         raise EcasqError(f"{name} must have at least one column and adjacent columns")
-    ld = t.stride(0) if n > 1 else k
-    if ld < k:
+    if n <= 1:
+        ld = k
+    elif ld < k:
         raise EcasqError(f"{name} has overlapping rows (stride {ld} for {k} columns)")
     return n, k, ld
 
 
-def _matrix8(t, name, dtype, to, device=None):
+def _matrix8(t, name, dtypes, to, index=None):
     """Checks a matrix of 8-bit values whose rows lie in a whole number of `to` bytes."""
-    n, k, ld = _matrix(t, name, (dtype,), device)
+    n, k, ld = _matrix(t, name, dtypes, index)
     if n <= 1:
         ld = (k + to - 1) // to * to
         whole = t.untyped_storage().nbytes() - t.storage_offset() >= n * ld
@@ -501,64 +516,102 @@ def _matrix8(t, name, dtype, to, device=None):
     return n, k, ld
 
 
-def _vector(t, name, dtype, n, device):
-    if t.dtype != dtype or t.dim() != 1 or t.shape[0] != n or t.device != device or (n > 1 and t.stride(0) != 1):
-        raise EcasqError(f"{name} must be a contiguous {dtype} tensor of {n} entries on {device}")
+_INT8, _UINT8 = (torch.int8,), (torch.uint8,)
+
+
+def _vector(t, name, n, index):
+    if t.dtype != torch.float32 or t.shape != (n,) or t.get_device() != index or not t.is_contiguous():
+        raise EcasqError(f"{name} must be a contiguous float32 tensor of {n} entries on cuda:{index}")
     return t.data_ptr()
 
 
 def _rows8(n, k, to, dtype, device):
-    """Uninitialised 8-bit values [n, k] in rows of a whole number of `to` bytes."""
-    return torch.empty((n, (k + to - 1) // to * to), dtype=dtype, device=device)
+    """Uninitialised 8-bit values in rows of a whole number of `to` bytes: all of them, and the [n, k] part."""
+    kp = (k + to - 1) // to * to
+    t = torch.empty((n, kp), dtype=dtype, device=device)
+    return t, (t if kp == k else t[:, :k])
 
 
-def _call(name, device, *args):
-    """One call of the library on the current stream of `device`."""
-    fn = getattr(_lib, name)
-    if device.index == torch.cuda.current_device():
-        rc = fn(*args, torch.cuda.current_stream().cuda_stream)
-    else:
-        with torch.cuda.device(device):
-            rc = fn(*args, torch.cuda.current_stream().cuda_stream)
-    _check(rc, name)
+def _elsewhere(index):
+    """Whether tensors on CUDA device `index` need it made current; also loads the library."""
+    if _lib is None or index < 0:
+        _need_cuda()
+    return index >= 0 and index != torch.cuda.current_device()
 
 
 def int8_quantize(X: torch.Tensor):
     """Rows of X (float32, bfloat16 or float16 [n, k]) in 8-bit integers with one
     scale per row: q int8 [n, k], scale float32 [n], status int32 [n], with
     X ~ q * scale[:, None] and q the nearest integers to 127 X / max |row|."""
-    _need_cuda()
+    index = X.get_device()
+    if _elsewhere(index):
+        with torch.cuda.device(index):
+            return int8_quantize(X)
     n, k, ld = _matrix(X, "X", _TYPES)
     dev = X.device
-    q = _rows8(n, k, 32, torch.int8, dev)
+    rows, q = _rows8(n, k, 32, torch.int8, dev)
     scale = torch.empty(n, dtype=torch.float32, device=dev)
     st = torch.empty(n, dtype=torch.int32, device=dev)
-    _call("ecasq_int8_quantize", dev, X.data_ptr(), _TYPES[X.dtype], n, k, ld, q.data_ptr(), q.shape[1],
-          scale.data_ptr(), st.data_ptr())
-    return q[:, :k], scale, st
+    rc = _lib.ecasq_int8_quantize(X.data_ptr(), _TYPES[X.dtype], n, k, ld, rows.data_ptr(), rows.shape[1],
+                                  scale.data_ptr(), st.data_ptr(), _stream_of(index))
+    if rc:
+        _check(rc, "ecasq_int8_quantize")
+    return q, scale, st
+
+
+def _weights(B, sb, bias, k, index):
+    """Checks 8-bit weights [n, k]; returns n, the row pitch and the addresses of sb and bias."""
+    n, kb, ldb = _matrix8(B, "B", _INT8, 16, index)
+    if kb != k:
+        raise EcasqError(f"the tokens have {k} columns and the weights {kb}")
+    if k > 131072:
+        raise EcasqError(f"sums of {k} products do not fit in 32 bits (at most 131072)")
+    if n < 1:
+        raise EcasqError("the weights must have at least one row")
+    return n, ldb, _vector(sb, "sb", n, index), None if bias is None else _vector(bias, "bias", n, index)
 
 
 def int8_matmul(A: torch.Tensor, sa: torch.Tensor, B: torch.Tensor, sb: torch.Tensor, bias=None,
                 out_dtype=torch.bfloat16):
     """Y [m, n] = (A B^T) * sa[:, None] * sb + bias from int8 A [m, k] (tokens) and
     B [n, k] (output channels) as int8_quantize returns them; bias float32 [n]."""
-    _need_cuda()
-    dev = A.device
-    m, k, lda = _matrix8(A, "A", torch.int8, 16)
-    n, kb, ldb = _matrix8(B, "B", torch.int8, 16, dev)
-    if kb != k:
-        raise EcasqError(f"A has {k} columns and B {kb}")
-    if k > 131072:
-        raise EcasqError(f"sums of {k} products do not fit in 32 bits (at most 131072)")
-    if n < 1:
-        raise EcasqError("B must have at least one row")
+    index = A.get_device()
+    if _elsewhere(index):
+        with torch.cuda.device(index):
+            return int8_matmul(A, sa, B, sb, bias, out_dtype)
+    m, k, lda = _matrix8(A, "A", _INT8, 16)
+    n, ldb, sbp, biasp = _weights(B, sb, bias, k, index)
     if out_dtype not in _TYPES:
         raise EcasqError(f"out_dtype must be float32, bfloat16 or float16, not {out_dtype}")
-    Y = torch.empty((m, n), dtype=out_dtype, device=dev)
-    _call("ecasq_int8_matmul", dev, A.data_ptr(), lda, _vector(sa, "sa", torch.float32, m, dev), B.data_ptr(), ldb,
-          _vector(sb, "sb", torch.float32, n, dev),
-          None if bias is None else _vector(bias, "bias", torch.float32, n, dev), m, n, k, Y.data_ptr(),
-          _TYPES[out_dtype], n)
+    Y = torch.empty((m, n), dtype=out_dtype, device=A.device)
+    rc = _lib.ecasq_int8_matmul(A.data_ptr(), lda, _vector(sa, "sa", m, index), B.data_ptr(), ldb, sbp, biasp, m, n, k,
+                                Y.data_ptr(), _TYPES[out_dtype], n, _stream_of(index))
+    if rc:
+        _check(rc, "ecasq_int8_matmul")
+    return Y
+
+
+@functools.lru_cache(maxsize=4096)
+def _linear_workspace(m, k):
+    return int(_lib.ecasq_int8_linear_workspace_size(m, k))
+
+
+def int8_linear(X: torch.Tensor, B: torch.Tensor, sb: torch.Tensor, bias=None):
+    """int8_quantize of the tokens X [m, k] and int8_matmul with the weights (B, sb,
+    bias) in one call, in X's type."""
+    index = X.get_device()
+    if _elsewhere(index):
+        with torch.cuda.device(index):
+            return int8_linear(X, B, sb, bias)
+    m, k, ld = _matrix(X, "X", _TYPES)
+    n, ldb, sbp, biasp = _weights(B, sb, bias, k, index)
+    Y = X.new_empty((m, n))
+    need = _linear_workspace(m, k)
+    ws = torch.empty(need, dtype=torch.uint8, device=X.device) if need else None
+    rc = _lib.ecasq_int8_linear(X.data_ptr(), _TYPES[X.dtype], ld, B.data_ptr(), ldb, sbp, biasp, m, n, k, Y.data_ptr(),
+                                n, ws.data_ptr() if need else None, need, _stream_of(index))
+    if rc:
+        _check(rc, "ecasq_int8_linear")
     return Y
 
 
@@ -567,25 +620,30 @@ def checkpoint8(X: torch.Tensor, seed):
     q int8 [t, k] and the scale bytes uint8 [t, ceil(k / 32)] of its blocks of 32
     entries. `seed` is an integer, or a CUDA int64 tensor of one entry read when
     the call runs (a graph's replays then draw new bits when it changes)."""
-    _need_cuda()
+    index = X.get_device()
+    if _elsewhere(index):
+        with torch.cuda.device(index):
+            return checkpoint8(X, seed)
     t, k, ld = _matrix(X, "X", _TYPES)
-    dev = X.device
     word = None
     if isinstance(seed, torch.Tensor):
-        if seed.dtype != torch.int64 or seed.numel() != 1 or seed.device != dev:
-            raise EcasqError(f"a seed tensor must hold one int64 on {dev}")
+        if seed.dtype != torch.int64 or seed.numel() != 1 or seed.get_device() != index:
+            raise EcasqError(f"a seed tensor must hold one int64 on cuda:{index}")
         seed, word = 0, seed.data_ptr()
-    blocks = (k + 31) // 32
-    q = _rows8(t, k, 32, torch.int8, dev)
-    s = _rows8(t, blocks, 16, torch.uint8, dev)
-    _call("ecasq_checkpoint8", dev, X.data_ptr(), _TYPES[X.dtype], t, k, ld, seed & 0xFFFFFFFFFFFFFFFF, word,
-          q.data_ptr(), q.shape[1], s.data_ptr(), s.shape[1])
-    return q[:, :k], s[:, :blocks]
+    dev = X.device
+    q_rows, q = _rows8(t, k, 32, torch.int8, dev)
+    s_rows, s = _rows8(t, (k + 31) // 32, 16, torch.uint8, dev)
+    rc = _lib.ecasq_checkpoint8(X.data_ptr(), _TYPES[X.dtype], t, k, ld, seed & 0xFFFFFFFFFFFFFFFF, word,
+                                q_rows.data_ptr(), q_rows.shape[1], s_rows.data_ptr(), s_rows.shape[1],
+                                _stream_of(index))
+    if rc:
+        _check(rc, "ecasq_checkpoint8")
+    return q, s
 
 
-def _checkpoint(q, scale):
-    t, k, ldq = _matrix8(q, "q", torch.int8, 32)
-    ts, blocks, lds = _matrix8(scale, "scale", torch.uint8, 16, q.device)
+def _checkpoint(q, scale, index=None):
+    t, k, ldq = _matrix8(q, "q", _INT8, 32, index)
+    ts, blocks, lds = _matrix8(scale, "scale", _UINT8, 16, q.get_device())
     if ts != t or blocks != (k + 31) // 32:
         raise EcasqError(f"scale must be [{t}, {(k + 31) // 32}] for q [{t}, {k}], not {list(scale.shape)}")
     return t, k, ldq, lds
@@ -593,35 +651,50 @@ def _checkpoint(q, scale):
 
 def checkpoint8_restore(q: torch.Tensor, scale: torch.Tensor, dtype=torch.float32):
     """The values of a checkpoint as a [t, k] tensor of dtype."""
-    _need_cuda()
+    index = q.get_device()
+    if _elsewhere(index):
+        with torch.cuda.device(index):
+            return checkpoint8_restore(q, scale, dtype)
     t, k, ldq, lds = _checkpoint(q, scale)
     if dtype not in _TYPES:
         raise EcasqError(f"dtype must be float32, bfloat16 or float16, not {dtype}")
     X = torch.empty((t, k), dtype=dtype, device=q.device)
-    _call("ecasq_checkpoint8_restore", q.device, q.data_ptr(), ldq, scale.data_ptr(), lds, t, k, X.data_ptr(),
-          _TYPES[dtype], k)
+    rc = _lib.ecasq_checkpoint8_restore(q.data_ptr(), ldq, scale.data_ptr(), lds, t, k, X.data_ptr(), _TYPES[dtype], k,
+                                        _stream_of(index))
+    if rc:
+        _check(rc, "ecasq_checkpoint8_restore")
     return X
+
+
+@functools.lru_cache(maxsize=4096)
+def _wgrad_workspace(index, offset, ty, ldy, t, o, k):
+    return int(_lib.ecasq_checkpoint8_wgrad_workspace_size(16 + offset, ty, ldy, t, o, k))
 
 
 def checkpoint8_wgrad(dY: torch.Tensor, q: torch.Tensor, scale: torch.Tensor, out_dtype=None):
     """dW [o, k] = dY^T X^ from dY [t, o] and the checkpoint (q, scale) of X [t, k];
     out_dtype is dY's unless given."""
-    L = _need_cuda()
-    dev = dY.device
+    index = dY.get_device()
+    if _elsewhere(index):
+        with torch.cuda.device(index):
+            return checkpoint8_wgrad(dY, q, scale, out_dtype)
     t, o, ldy = _matrix(dY, "dY", _TYPES)
-    tq, k, ldq, lds = _checkpoint(q, scale)
-    if tq != t or q.device != dev:
-        raise EcasqError(f"dY has {t} rows on {dev}, the checkpoint {tq} on {q.device}")
-    out_dtype = dY.dtype if out_dtype is None else out_dtype
-    if out_dtype not in _TYPES:
-        raise EcasqError(f"out_dtype must be float32, bfloat16 or float16, not {out_dtype}")
-    dW = torch.empty((o, k), dtype=out_dtype, device=dev)
+    tq, k, ldq, lds = _checkpoint(q, scale, index)
+    if tq != t:
+        raise EcasqError(f"dY has {t} rows and the checkpoint {tq}")
     ty = _TYPES[dY.dtype]
-    need = L.ecasq_checkpoint8_wgrad_workspace_size(dY.data_ptr(), ty, ldy, t, o, k)
-    # the caching allocator's, so that it belongs to this call (or to the graph that captures it) alone
-    ws = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
-    _call("ecasq_checkpoint8_wgrad", dev, dY.data_ptr(), ty, ldy, q.data_ptr(), ldq, scale.data_ptr(), lds, t, o, k,
-          dW.data_ptr(), _TYPES[out_dtype], k, ws.data_ptr() if need else None, need)
+    if out_dtype is None:
+        out_dtype = dY.dtype
+    elif out_dtype not in _TYPES:
+        raise EcasqError(f"out_dtype must be float32, bfloat16 or float16, not {out_dtype}")
+    dW = torch.empty((o, k), dtype=out_dtype, device=dY.device)
+    at = dY.data_ptr()
+    need = _wgrad_workspace(index, at % 16, ty, ldy, t, o, k)
+    ws = torch.empty(need, dtype=torch.uint8, device=dY.device) if need else None
+    rc = _lib.ecasq_checkpoint8_wgrad(at, ty, ldy, q.data_ptr(), ldq, scale.data_ptr(), lds, t, o, k, dW.data_ptr(),
+                                      _TYPES[out_dtype], k, ws.data_ptr() if need else None, need, _stream_of(index))
+    if rc:
+        _check(rc, "ecasq_checkpoint8_wgrad")
     return dW
 
 

@@ -24,12 +24,12 @@ def int8_linear(x: torch.Tensor, weight: torch.Tensor, weight_scale: torch.Tenso
     weight_scale float32 [n] are ecasq.int8_quantize's of the layer's weight
     matrix; bias float32 [n]. For serving: it has no gradient, and refuses an x
     that asks for one."""
-    if torch.is_grad_enabled() and x.requires_grad:
+    if x.requires_grad and torch.is_grad_enabled():
         raise E.EcasqError("int8_linear has no gradient; use checkpoint_linear for training, or torch.no_grad()")
-    rows = x if x.dim() == 2 else x.reshape(-1, x.shape[-1])
-    q, scale, _ = E.int8_quantize(rows)
-    y = E.int8_matmul(q, scale, weight, weight_scale, bias, x.dtype)
-    return y if x.dim() == 2 else y.reshape(*x.shape[:-1], y.shape[1])
+    if x.dim() == 2:
+        return E.int8_linear(x, weight, weight_scale, bias)
+    y = E.int8_linear(x.reshape(-1, x.shape[-1]), weight, weight_scale, bias)
+    return y.reshape(*x.shape[:-1], y.shape[1])
 
 
 class _CheckpointLinear(torch.autograd.Function):

@@ -354,6 +354,16 @@ int ecasq_int8_matmul(const int8_t* A, int64_t lda, const float* sa, const int8_
                       const float* bias, int64_t m, int64_t n, int64_t k, void* Y, int y_type, int64_t ldy,
                       void* stream);
 
+/* ecasq_int8_quantize of the tokens X [m][k] and ecasq_int8_matmul with the weights
+ * (B, sb, bias), with the same results; Y is in X's type. A token holding a NaN or
+ * an infinity gives a row of NaN. The workspace (16-byte aligned,
+ * ecasq_int8_linear_workspace_size bytes; 0 for few tokens) holds the quantised
+ * tokens. */
+size_t ecasq_int8_linear_workspace_size(int64_t m, int64_t k);
+int ecasq_int8_linear(const void* X, int x_type, int64_t ldx, const int8_t* B, int64_t ldb, const float* sb,
+                      const float* bias, int64_t m, int64_t n, int64_t k, void* Y, int64_t ldy, void* ws,
+                      size_t ws_bytes, void* stream);
+
 /* Activation checkpoint in 8 bits. Each row of X [t][k] is cut into blocks of
  * 32 entries (the last one may be short); a block's scale s is the smallest
  * power of two, at least 2^-126, with max |x| <= 127 s, stored as the byte b

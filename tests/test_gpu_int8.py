@@ -163,6 +163,28 @@ def test_linear_keeps_leading_dimensions_and_type(E, shape):
         assert torch.equal(y.reshape(-1, 40), E.int8_matmul(q, s, wq, ws, None, torch.float16))
 
 
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("m,n,k", [(1, 1, 1), (1, 300, 4099), (2, 65, 16384), (3, 129, 100), (5, 7, 33), (8, 1000, 520),
+                                   (7, 9000, 64), (8, 40, 20000), (1, 33, 131072), (9, 100, 70), (40, 200, 1000)])
+def test_linear_equals_its_two_steps(E, m, n, k, dtype):
+    """One call gives what quantising and multiplying give, bit for bit, from few tokens (one kernel) to many."""
+    w = _x(n, n, k, torch.float32)
+    wq, ws, _ = E.int8_quantize(w)
+    bias = torch.randn(n, generator=torch.Generator().manual_seed(2)).cuda()
+    x = _x(m + k, m, k, dtype)
+    if m > 2:
+        x[1] = 0
+        x[2, k // 2] = float("nan")
+    q, s, _ = E.int8_quantize(x)
+    for b in (None, bias):
+        y, z = E.int8_linear(x, wq, ws, b), E.int8_matmul(q, s, wq, ws, b, dtype)
+        assert y.dtype == dtype and torch.equal(y.nan_to_num(7.0), z.nan_to_num(7.0))
+        assert torch.isnan(y).any() == (m > 2)
+    off = torch.empty((m, k + 3), dtype=dtype, device="cuda")
+    off[:, 3:] = x
+    assert torch.equal(E.int8_linear(off[:, 3:], wq, ws).nan_to_num(7.0), E.int8_linear(x, wq, ws).nan_to_num(7.0))
+
+
 def test_linear_refuses_a_gradient(E):
     from entropy_constrained_unbiased_b200.linear import int8_linear
     wq, ws, _ = E.int8_quantize(_x(9, 40, 64, torch.float32))

@@ -37,6 +37,24 @@ def test_matmul_arguments(lib):
     assert f(NULL, 0, NULL, NULL, 0, NULL, NULL, 0, 8, 100, NULL, 1, 8, NULL) == 0
 
 
+def test_linear_arguments(lib):
+    f = lib.ecasq_int8_linear
+    good = [P16, 1, 100, P16, 112, P16, NULL, 40, 8, 100, P16, 8, P16, 1 << 20, NULL]
+    for at, bad in [(0, NULL), (1, 4), (2, 99), (3, NULL), (3, ODD), (4, 104), (5, NULL), (7, -1), (8, 0), (9, 0), (9, 131073),
+                    (10, NULL), (11, 7)]:
+        args = list(good)
+        args[at] = bad
+        assert f(*args) == -1, (at, bad)
+    need = lib.ecasq_int8_linear_workspace_size(40, 100)
+    assert need >= 40 * (128 + 4)
+    for at, bad in [(12, NULL), (12, ODD), (13, need - 1)]:
+        args = list(good)
+        args[at] = bad
+        assert f(*args) == -3, (at, bad)
+    assert f(NULL, 1, 100, NULL, 0, NULL, NULL, 0, 8, 100, NULL, 8, NULL, 0, NULL) == 0
+    assert lib.ecasq_int8_linear_workspace_size(-1, 100) == 0 and lib.ecasq_int8_linear_workspace_size(4, 0) == 0
+
+
 def test_checkpoint_arguments(lib):
     f = lib.ecasq_checkpoint8
     good = [P16, 0, 4, 100, 100, 7, NULL, P16, 128, P16, 16, NULL]
@@ -74,7 +92,7 @@ def test_no_cpu_path():
     q, s = torch.zeros((2, 32), dtype=torch.int8), torch.zeros(2)
     for call in (lambda: E.int8_quantize(x), lambda: E.int8_matmul(q, s, q, s), lambda: E.checkpoint8(x, 1),
                  lambda: E.checkpoint8_restore(q, q.view(torch.uint8)), lambda: int8_linear(x, q, s),
-                 lambda: E.checkpoint8_wgrad(x, q, q.view(torch.uint8)), lambda: checkpoint_linear(x, x, seed=1)):
+                 lambda: E.checkpoint8_wgrad(x, q, q.view(torch.uint8)), lambda: checkpoint_linear(x, x, seed=1), lambda: E.int8_linear(x, q, s)):
         with pytest.raises(E.EcasqError):
             call()
 
