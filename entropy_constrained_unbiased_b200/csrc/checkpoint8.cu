@@ -130,13 +130,18 @@ constexpr int kOperand = kTok * 128 * 2;  // bf16 operand of one CTA: 128 featur
 constexpr int kHalf = kTok * 64 * 2;      // its 64-wide half (one swizzle atom across)
 constexpr int kInts = kTok * 128;         // integers of 128 features
 constexpr int kScales = kTok * 16;        // scale bytes of 512 features
-constexpr int kXStage = kOperand + kInts + kScales;
-constexpr int kXStages = 4, kYStages = 7;
-constexpr int kGradSmem = kXStages * kXStage + kYStages * kOperand + 1024;
+constexpr int kQStage = kInts + kScales;
+// Stages of integers, of converted X^ and of dY. A stage of 64 tokens keeps the tensor
+// cores busy for 512 clocks and its loads take two to four times as long.
+constexpr int kQStages = 7, kXStages = 4, kYStages = 6;
+constexpr int kGradSmem = kQStages * kQStage + kXStages * kOperand + kYStages * kOperand + 1024;
 
-// Warps: the epilogue's, the producer, the MMA issuer, the converters. kExact holds
-// 128 sums a thread in the epilogue's registers, so its warps come in groups of four
-// that trade registers (setmaxnreg): 256 * 184 + 256 * 72 = 512 * 128.
+// Warps: the epilogue's, the producer, the MMA issuer, the converters. The converters
+// come in kXStages groups that take the stages in turn, so that the latencies of one
+// stage's conversion (its wait, its loads, the fence, the arrival at the other CTA)
+// are covered by three others'. kExact holds 128 sums a thread in the epilogue's
+// registers, so its warps come in groups of four that trade registers (setmaxnreg):
+// 256 * 184 + 256 * 72 = 512 * 128.
 template <bool kExact>
 struct GradWarps {
   static constexpr int kEpilogue = kExact ? 8 : 4;
@@ -187,15 +192,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GradWarps<kExact>::k
             const __grid_constant__ CUtensorMap map_y, const Gradient g) {
   using W = GradWarps<kExact>;
   extern __shared__ unsigned char smem_raw[];
-  __shared__ uint64_t bars[3 * kXStages + 2 * kYStages + 4];
+  __shared__ uint64_t bars[2 * kQStages + 2 * kXStages + 2 * kYStages + 4];
   __shared__ uint32_t tmem_slot;
-  const uint32_t xs = (smem_addr(smem_raw) + 1023) & ~1023u, ys = xs + kXStages * kXStage;
-  // integers and scales here (own CTA), X^ converted (both CTAs, on the even one), X^
-  // read by the MMAs; dY here (both CTAs, on the even one), dY read; per accumulator:
-  // done, freed
-  const uint32_t ints = smem_addr(bars), ready = ints + 8 * kXStages, x_empty = ready + 8 * kXStages,
-                 full = x_empty + 8 * kXStages, y_empty = full + 8 * kYStages, done = y_empty + 8 * kYStages,
-                 freed = done + 16;
+  const uint32_t xs = (smem_addr(smem_raw) + 1023) & ~1023u, ys = xs + kXStages * kOperand, qs = ys + kYStages * kOperand;
+  // integers and scales here, and read (own CTA); X^ converted (both CTAs, on the even
+  // one), X^ read by the MMAs; dY here (both CTAs, on the even one), dY read; per
+  // accumulator: done, freed
+  const uint32_t ints = smem_addr(bars), q_empty = ints + 8 * kQStages, ready = q_empty + 8 * kQStages,
+                 x_empty = ready + 8 * kXStages, full = x_empty + 8 * kXStages, y_empty = full + 8 * kYStages,
+                 done = y_empty + 8 * kYStages, freed = done + 16;
+  constexpr int kGroup = W::kConvert / kXStages;  // warps that convert one stage
   const int warp = warp_id(), lane = lane_id();
   const int rank = static_cast<int>(cluster_rank());
   const int pair = static_cast<int>(blockIdx.x) >> 1, pairs = static_cast<int>(gridDim.x) >> 1;
@@ -207,9 +213,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GradWarps<kExact>::k
     prefetch_map(&map_q);
     prefetch_map(&map_s);
     prefetch_map(&map_y);
-    for (int i = 0; i < kXStages; ++i) {
+    for (int i = 0; i < kQStages; ++i) {
       mbar_init(ints + 8 * i, 1);
-      mbar_init(ready + 8 * i, 2 * W::kConvert);
+      mbar_init(q_empty + 8 * i, kGroup);
+    }
+    for (int i = 0; i < kXStages; ++i) {
+      mbar_init(ready + 8 * i, 2 * kGroup);
       mbar_init(x_empty + 8 * i, 1);
     }
     for (int i = 0; i < kYStages; ++i) {
@@ -232,106 +241,108 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GradWarps<kExact>::k
     if constexpr (kExact) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
     if (warp == W::kLoad && lane == 0) {
       const uint32_t full0 = map_shared(full, 0);
-      int64_t ix = 0, iy = 0;
+      Ring<kQStages> q;
+      Ring<kYStages> y;
       for (int w = pair; w < all && ok; w += pairs) {
         const int tile = w % tiles, part = w / tiles;
         const int f0 = (tile % g.feature_tiles) * 256 + rank * 128, o0 = (tile / g.feature_tiles) * 256 + rank * 128;
         const int last = min(g.pieces, (part + 1) * g.per);
-        for (int i = part * g.per; i < last && ok; ++i, ++ix) {
-          const int s = static_cast<int>(ix % kXStages);
-          if (ix >= kXStages) ok = mbar_wait_bounded(x_empty + 8 * s, (ix / kXStages + 1) & 1, kWaitLimit);
+        for (int i = part * g.per; i < last && ok; ++i, q.next()) {
+          ok = q.wait_empty(q_empty, kWaitLimit);
           if (!ok) break;
-          const uint32_t q = xs + s * kXStage + kOperand;
-          mbar_expect_tx(ints + 8 * s, kInts + kScales);
-          tma_2d(q, &map_q, f0, i * kTok, ints + 8 * s);
-          tma_2d(q + kInts, &map_s, (f0 / 32) & ~15, i * kTok, ints + 8 * s);
-          for (int term = 0; term < g.terms; ++term, ++iy) {
-            const int y = static_cast<int>(iy % kYStages);
-            if (iy >= kYStages) ok = mbar_wait_bounded(y_empty + 8 * y, (iy / kYStages + 1) & 1, kWaitLimit);
+          const uint32_t to = qs + q.stage * kQStage, bar = ints + 8 * q.stage;
+          mbar_expect_tx(bar, kInts + kScales);
+          tma_2d(to, &map_q, f0, i * kTok, bar);
+          tma_2d(to + kInts, &map_s, (f0 / 32) & ~15, i * kTok, bar);
+          for (int term = 0; term < g.terms; ++term, y.next()) {
+            ok = y.wait_empty(y_empty, kWaitLimit);
             if (!ok) break;
-            if (rank == 0) mbar_expect_tx(full + 8 * y, 2 * kOperand);
-            tma_3d_pair(ys + y * kOperand, &map_y, o0, i * kTok, term, full0 + 8 * y);
-            tma_3d_pair(ys + y * kOperand + kHalf, &map_y, o0 + 64, i * kTok, term, full0 + 8 * y);
+            const uint32_t there = ys + y.stage * kOperand, bar_y = full0 + 8 * y.stage;
+            if (rank == 0) mbar_expect_tx(full + 8 * y.stage, 2 * kOperand);
+            tma_3d_pair(there, &map_y, o0, i * kTok, term, bar_y);
+            tma_3d_pair(there + kHalf, &map_y, o0 + 64, i * kTok, term, bar_y);
           }
         }
       }
-      if (!ok) {  // wait for the copies in flight before the memory is given back
-        for (int64_t i = ix > kXStages ? ix - kXStages : 0; i < ix; ++i)
-          mbar_wait_bounded(ints + 8 * static_cast<uint32_t>(i % kXStages), (i / kXStages) & 1, kWaitLimit);
-        for (int64_t i = iy > kYStages ? iy - kYStages : 0; i < iy && rank == 0; ++i)
-          mbar_wait_bounded(full + 8 * static_cast<uint32_t>(i % kYStages), (i / kYStages) & 1, kWaitLimit);
+      if (!ok) {  // before the memory is given back
+        q.drain(ints, kWaitLimit);
+        if (rank == 0) y.drain(full, kWaitLimit);
       }
     } else if (warp == W::kIssue && lane == 0 && rank == 0) {
-      int64_t ix = 0, iy = 0;
-      int n = 0;  // accumulators begun
+      Ring<kXStages> x;
+      Ring<kYStages> y;
+      Ring<2> out;
       for (int w = pair; w < all && ok; w += pairs) {
         const int part = w / tiles;
         const int count = min(g.pieces, (part + 1) * g.per) - part * g.per;
-        for (int i = 0; i < count && ok; ++n) {
-          const int buf = n & 1;
-          if (n >= 2) ok = mbar_wait_bounded(freed + 8 * buf, ((n >> 1) + 1) & 1, kWaitLimit);
+        for (int i = 0; i < count && ok; out.next()) {
+          ok = out.wait_empty(freed, kWaitLimit);
           if (!ok) break;
           tcgen05_after_sync();
           const int end = min(count, i + g.chunk);
-          for (bool add = false; i < end && ok; ++i, ++ix) {
-            const int s = static_cast<int>(ix % kXStages);
-            ok = mbar_wait_bounded(ready + 8 * s, (ix / kXStages) & 1, kWaitLimit);
-            const uint64_t da = smem_desc(xs + s * kXStage, kHalf, 1024);
-            for (int term = 0; term < g.terms && ok; ++term, ++iy) {
-              const int y = static_cast<int>(iy % kYStages);
-              ok = mbar_wait_bounded(full + 8 * y, (iy / kYStages) & 1, kWaitLimit);
+          for (bool add = false; i < end && ok; ++i, x.next()) {
+            ok = x.wait_full(ready, kWaitLimit);
+            const uint64_t da = smem_desc(xs + x.stage * kOperand, kHalf, 1024);
+            for (int term = 0; term < g.terms && ok; ++term, y.next()) {
+              ok = y.wait_full(full, kWaitLimit);
               if (!ok) break;
               tcgen05_after_sync();
-              const uint64_t db = smem_desc(ys + y * kOperand, kHalf, 1024);
+              const uint64_t db = smem_desc(ys + y.stage * kOperand, kHalf, 1024);
 #pragma unroll
               for (int j = 0; j < kTok / 16; ++j) {  // 16 tokens per MMA: 16 rows of 128 bytes
-                mma_bf16<2>(acc + buf * 256, da + j * (2048 >> 4), db + j * (2048 >> 4), idesc_bf16_mn(256, 256), add);
+                mma_bf16<2>(acc + out.stage * 256, da + j * (2048 >> 4), db + j * (2048 >> 4), idesc_bf16_mn(256, 256), add);
                 add = true;
               }
-              mma_commit<2>(y_empty + 8 * y);
+              mma_commit<2>(y_empty + 8 * y.stage);
             }
-            mma_commit<2>(x_empty + 8 * s);
+            mma_commit<2>(x_empty + 8 * x.stage);
           }
-          mma_commit<2>(done + 8 * buf);
+          mma_commit<2>(done + 8 * out.stage);
         }
       }
     } else if (warp >= W::kConvert0) {
-      constexpr int kRows = kTok / W::kConvert;  // tokens of one warp
+      constexpr int kRows = kTok / kGroup;  // tokens of one warp
       const uint32_t ready0 = map_shared(ready, 0);
-      const int row = (warp - W::kConvert0) * kRows + (lane >> 3), chunk = lane & 7;
+      const uint32_t group = (warp - W::kConvert0) / kGroup;  // and the X^ stage that it fills
+      const int row = (warp - W::kConvert0) % kGroup * kRows + (lane >> 3), chunk = lane & 7;
       // 16-byte pieces 2c and 2c + 1 of a 128-byte row, swizzled by the row; the upper 64
       // features write theirs in the other order, so that the eight threads of a row
       // hit different banks
       const int half = chunk >> 2, c = (chunk & 3) * 2;
-      int64_t ix = 0;
+      const uint32_t to = xs + group * kOperand + half * kHalf + row * 128;
+      Ring<kQStages> q;
+      Ring<kXStages> x;
       for (int w = pair; w < all && ok; w += pairs) {
         const int tile = w % tiles, part = w / tiles;
         const int f0 = (tile % g.feature_tiles) * 256 + rank * 128;
         const uint32_t block = ((f0 / 32) & 15) + (chunk >> 1);
         const int count = min(g.pieces, (part + 1) * g.per) - part * g.per;
-        for (int i = 0; i < count; ++i, ++ix) {
-          const int s = static_cast<int>(ix % kXStages);
-          ok = __all_sync(0xffffffffu, mbar_wait_bounded(ints + 8 * s, (ix / kXStages) & 1, kWaitLimit));
+        for (int i = 0; i < count; ++i, q.next(), x.next()) {
+          if (x.stage != group) continue;
+          ok = __all_sync(0xffffffffu, q.wait_full(ints, kWaitLimit) && x.wait_empty(x_empty, kWaitLimit));
           if (!ok) break;
-          const uint32_t to = xs + s * kXStage, from = to + kOperand;
-#pragma unroll
+          const uint32_t from = qs + q.stage * kQStage + row * 128 + chunk * 16;
+          const uint32_t scales = qs + q.stage * kQStage + kInts + row * 16 + block;
+#pragma unroll 4
           for (int r = 0; r < kRows; r += 4) {
-            const int t = row + r;
-            const uint4 x = ld_shared16(from + t * 128 + chunk * 16);
-            const uint32_t b = ld_shared1(from + kInts + t * 16 + block);
+            const uint4 x = ld_shared16(from + r * 128);
+            const uint32_t b = ld_shared1(scales + r * 16);
             const uint32_t bits = (b == kScaleNaN ? 0x7FFFu : b << 7) * 0x10001u;
             const __nv_bfloat162 sc = *reinterpret_cast<const __nv_bfloat162*>(&bits);
             const uint4 v0 = make_uint4(two_values(x.x, 0x4140, sc), two_values(x.x, 0x4342, sc),
                                         two_values(x.y, 0x4140, sc), two_values(x.y, 0x4342, sc));
             const uint4 v1 = make_uint4(two_values(x.z, 0x4140, sc), two_values(x.z, 0x4342, sc),
                                         two_values(x.w, 0x4140, sc), two_values(x.w, 0x4342, sc));
-            const uint32_t line = to + half * kHalf + t * 128;
-            st_shared16(line + (((c + half) ^ (t & 7)) << 4), half ? v1 : v0);
-            st_shared16(line + (((c + 1 - half) ^ (t & 7)) << 4), half ? v0 : v1);
+            const int swizzle = (row + r) & 7;
+            st_shared16(to + r * 128 + (((c + half) ^ swizzle) << 4), half ? v1 : v0);
+            st_shared16(to + r * 128 + (((c + 1 - half) ^ swizzle) << 4), half ? v0 : v1);
           }
           fence_proxy_async_shared();
           __syncwarp();
-          if (lane == 0) mbar_arrive_cluster(ready0 + 8 * s);
+          if (lane == 0) {
+            mbar_arrive_cluster(ready0 + 8 * group);
+            mbar_arrive(q_empty + 8 * q.stage);
+          }
         }
       }
     }

@@ -221,35 +221,30 @@ __global__ void __launch_bounds__(192, 2)
 
   if (warp == 4) {
     if (lane == 0) {
-      int loaded = 0;
-      for (; loaded < count && ok; ++loaded) {
-        const int s = loaded % Cfg::kStages;
-        if (loaded >= Cfg::kStages) {
-          ok = mbar_wait_bounded(empty + 8 * s, (loaded / Cfg::kStages + 1) & 1, kWaitLimit);
-          if (!ok) break;
-        }
-        const uint32_t a = tiles + s * (Cfg::kA + Cfg::kB);
-        mbar_expect_tx(full + 8 * s, Cfg::kA + Cfg::kB);
-        tma_2d(a, &map_w, (first + loaded) * kPieceK, channel0, full + 8 * s);
-        tma_2d(a + Cfg::kA, &map_x, (first + loaded) * kPieceK, token0, full + 8 * s);
+      Ring<Cfg::kStages> at;
+      for (int i = 0; i < count; ++i, at.next()) {
+        ok = at.wait_empty(empty, kWaitLimit);
+        if (!ok) break;
+        const uint32_t a = tiles + at.stage * (Cfg::kA + Cfg::kB), bar = full + 8 * at.stage;
+        mbar_expect_tx(bar, Cfg::kA + Cfg::kB);
+        tma_2d(a, &map_w, (first + i) * kPieceK, channel0, bar);
+        tma_2d(a + Cfg::kA, &map_x, (first + i) * kPieceK, token0, bar);
       }
-      if (!ok)  // wait for the copies in flight before the memory is given back
-        for (int i = max(0, loaded - Cfg::kStages); i < loaded; ++i)
-          mbar_wait_bounded(full + 8 * (i % Cfg::kStages), (i / Cfg::kStages) & 1, kWaitLimit);
+      if (!ok) at.drain(full, kWaitLimit);  // before the memory is given back
     }
   } else if (warp == 5) {
     if (lane == 0) {
-      for (int i = 0; i < count && ok; ++i) {
-        const int s = i % Cfg::kStages;
-        ok = mbar_wait_bounded(full + 8 * s, (i / Cfg::kStages) & 1, kWaitLimit);
+      Ring<Cfg::kStages> at;
+      for (int i = 0; i < count; ++i, at.next()) {
+        ok = at.wait_full(full, kWaitLimit);
         if (!ok) break;
         tcgen05_after_sync();
-        const uint32_t a = tiles + s * (Cfg::kA + Cfg::kB);
+        const uint32_t a = tiles + at.stage * (Cfg::kA + Cfg::kB);
         const uint64_t da = smem_desc(a, 16, 1024), db = smem_desc(a + Cfg::kA, 16, 1024);
 #pragma unroll
         for (int j = 0; j < kPieceK / kStepK; ++j)
           mma_i8<1>(acc, da + j * (kStepK >> 4), db + j * (kStepK >> 4), idesc_i8(128, kTok), i > 0 || j > 0);
-        mma_commit<1>(empty + 8 * s);
+        mma_commit<1>(empty + 8 * at.stage);
       }
       mma_commit<1>(done);
     }
@@ -391,50 +386,41 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(192, 1)
   if (warp == 4) {
     if (lane == 0) {
       const uint32_t full0 = map_shared(full, 0);
-      int64_t it = 0;
+      Ring<kPairStages> at;
       for (int t = pair; t < all && ok; t += pairs) {
-        const TileAt at = tile_at(t, channel_tiles, token_tiles);
-        const int c0 = at.channel * 256 + rank * 128, t0 = at.token * 256 + rank * 128;
-        for (int i = 0; i < p.pieces; ++i, ++it) {
-          const int s = static_cast<int>(it % kPairStages);
-          if (it >= kPairStages) {
-            ok = mbar_wait_bounded(empty + 8 * s, (it / kPairStages + 1) & 1, kWaitLimit);
-            if (!ok) break;
-          }
-          const uint32_t a = tiles + s * kPairStage;
-          if (rank == 0) mbar_expect_tx(full + 8 * s, 2 * kPairStage);
-          tma_2d_pair(a, &map_w, i * kPieceK, c0, full0 + 8 * s);
-          tma_2d_pair(a + 128 * kPieceK, &map_x, i * kPieceK, t0, full0 + 8 * s);
+        const TileAt tile = tile_at(t, channel_tiles, token_tiles);
+        const int c0 = tile.channel * 256 + rank * 128, t0 = tile.token * 256 + rank * 128;
+        for (int i = 0; i < p.pieces; ++i, at.next()) {
+          ok = at.wait_empty(empty, kWaitLimit);
+          if (!ok) break;
+          const uint32_t a = tiles + at.stage * kPairStage, bar = full0 + 8 * at.stage;
+          if (rank == 0) mbar_expect_tx(full + 8 * at.stage, 2 * kPairStage);
+          tma_2d_pair(a, &map_w, i * kPieceK, c0, bar);
+          tma_2d_pair(a + 128 * kPieceK, &map_x, i * kPieceK, t0, bar);
         }
       }
-      if (!ok && rank == 0)
-        for (int64_t i = it > kPairStages ? it - kPairStages : 0; i < it; ++i)
-          mbar_wait_bounded(full + 8 * static_cast<uint32_t>(i % kPairStages), (i / kPairStages) & 1, kWaitLimit);
+      if (!ok && rank == 0) at.drain(full, kWaitLimit);
     }
   } else if (warp == 5) {
     if (lane == 0 && rank == 0) {
-      int64_t it = 0;
-      int n = 0;
-      for (int t = pair; t < all && ok; t += pairs, ++n) {
-        const int buf = n & 1;
-        if (n >= 2) {
-          ok = mbar_wait_bounded(freed + 8 * buf, ((n >> 1) + 1) & 1, kWaitLimit);
-          if (!ok) break;
-        }
+      Ring<kPairStages> at;
+      Ring<2> out;
+      for (int t = pair; t < all && ok; t += pairs, out.next()) {
+        ok = out.wait_empty(freed, kWaitLimit);
+        if (!ok) break;
         tcgen05_after_sync();
-        for (int i = 0; i < p.pieces; ++i, ++it) {
-          const int s = static_cast<int>(it % kPairStages);
-          ok = mbar_wait_bounded(full + 8 * s, (it / kPairStages) & 1, kWaitLimit);
+        for (int i = 0; i < p.pieces; ++i, at.next()) {
+          ok = at.wait_full(full, kWaitLimit);
           if (!ok) break;
           tcgen05_after_sync();
-          const uint32_t a = tiles + s * kPairStage;
+          const uint32_t a = tiles + at.stage * kPairStage;
           const uint64_t da = smem_desc(a, 16, 1024), db = smem_desc(a + 128 * kPieceK, 16, 1024);
 #pragma unroll
           for (int j = 0; j < kPieceK / kStepK; ++j)
-            mma_i8<2>(acc + buf * 256, da + j * (kStepK >> 4), db + j * (kStepK >> 4), idesc_i8(256, 256), i > 0 || j > 0);
-          mma_commit<2>(empty + 8 * s);
+            mma_i8<2>(acc + out.stage * 256, da + j * (kStepK >> 4), db + j * (kStepK >> 4), idesc_i8(256, 256), i > 0 || j > 0);
+          mma_commit<2>(empty + 8 * at.stage);
         }
-        mma_commit<2>(done + 8 * buf);
+        mma_commit<2>(done + 8 * out.stage);
       }
     }
   } else {

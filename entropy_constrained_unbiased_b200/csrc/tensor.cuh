@@ -82,6 +82,35 @@ __device__ __forceinline__ void mbar_arrive_cluster(uint32_t mbar) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(mbar) : "memory");
 }
 
+// A place in a ring of kStages stages, walked in order: the stage, the parity of the
+// current round, and whether it is the first one. (Divisions of a running count cost
+// a single-threaded role hundreds of clocks per stage.)
+template <int kStages>
+struct Ring {
+  uint32_t stage = 0, parity = 0;
+  bool first = true;
+  __device__ __forceinline__ void next() {
+    if (++stage == kStages) {
+      stage = 0;
+      parity ^= 1;
+      first = false;
+    }
+  }
+  // Waits until the stage's last use is over (nothing to wait for in the first round).
+  __device__ __forceinline__ bool wait_empty(uint32_t bars, int limit) const {
+    return first || mbar_wait_bounded(bars + 8 * stage, parity ^ 1, limit);
+  }
+  __device__ __forceinline__ bool wait_full(uint32_t bars, int limit) const {
+    return mbar_wait_bounded(bars + 8 * stage, parity, limit);
+  }
+  // After a wait gave up: waits for the loads of every stage begun before this place.
+  __device__ __forceinline__ void drain(uint32_t bars, int limit) const {
+    if (!first)
+      for (uint32_t i = stage; i < kStages; ++i) mbar_wait_bounded(bars + 8 * i, parity ^ 1, limit);
+    for (uint32_t i = 0; i < stage; ++i) mbar_wait_bounded(bars + 8 * i, parity, limit);
+  }
+};
+
 // ---- device: TMA tile loads ------------------------------------------------------
 
 __device__ __forceinline__ void prefetch_map(const CUtensorMap* map) {
