@@ -202,7 +202,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GradWarps<kExact>::k
                  x_empty = ready + 8 * kXStages, full = x_empty + 8 * kXStages, y_empty = full + 8 * kYStages,
                  done = y_empty + 8 * kYStages, freed = done + 16;
   constexpr int kGroup = W::kConvert / kXStages;  // warps that convert one stage
-  const int warp = warp_id(), lane = lane_id();
+  const int warp = __shfl_sync(0xffffffffu, warp_id(), 0), lane = lane_id();
   const int rank = static_cast<int>(cluster_rank());
   const int pair = static_cast<int>(blockIdx.x) >> 1, pairs = static_cast<int>(gridDim.x) >> 1;
   const int tiles = g.feature_tiles * g.output_tiles;
@@ -234,12 +234,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GradWarps<kExact>::k
   tcgen05_before_sync();
   cluster_sync_all();
   tcgen05_after_sync();
-  const uint32_t acc = tmem_slot;
+  const uint32_t acc = __shfl_sync(0xffffffffu, tmem_slot, 0);
   bool ok = true;
 
   if (warp >= W::kEpilogue) {
     if constexpr (kExact) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
-    if (warp == W::kLoad && lane == 0) {
+    if (warp == W::kLoad) {
+      const bool elected = elect_one();
       const uint32_t full0 = map_shared(full, 0);
       Ring<kQStages> q;
       Ring<kYStages> y;
@@ -248,19 +249,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GradWarps<kExact>::k
         const int f0 = (tile % g.feature_tiles) * 256 + rank * 128, o0 = (tile / g.feature_tiles) * 256 + rank * 128;
         const int last = min(g.pieces, (part + 1) * g.per);
         for (int i = part * g.per; i < last && ok; ++i, q.next()) {
-          ok = q.wait_empty(q_empty, kWaitLimit);
+          ok = __all_sync(0xffffffffu, q.wait_empty(q_empty, kWaitLimit));
           if (!ok) break;
           const uint32_t to = qs + q.stage * kQStage, bar = ints + 8 * q.stage;
-          mbar_expect_tx(bar, kInts + kScales);
-          tma_2d(to, &map_q, f0, i * kTok, bar);
-          tma_2d(to + kInts, &map_s, (f0 / 32) & ~15, i * kTok, bar);
+          if (elected) {
+            mbar_expect_tx(bar, kInts + kScales);
+            tma_2d(to, &map_q, f0, i * kTok, bar);
+            tma_2d(to + kInts, &map_s, (f0 / 32) & ~15, i * kTok, bar);
+          }
           for (int term = 0; term < g.terms; ++term, y.next()) {
-            ok = y.wait_empty(y_empty, kWaitLimit);
+            ok = __all_sync(0xffffffffu, y.wait_empty(y_empty, kWaitLimit));
             if (!ok) break;
             const uint32_t there = ys + y.stage * kOperand, bar_y = full0 + 8 * y.stage;
-            if (rank == 0) mbar_expect_tx(full + 8 * y.stage, 2 * kOperand);
-            tma_3d_pair(there, &map_y, o0, i * kTok, term, bar_y);
-            tma_3d_pair(there + kHalf, &map_y, o0 + 64, i * kTok, term, bar_y);
+            if (elected) {
+              if (rank == 0) mbar_expect_tx(full + 8 * y.stage, 2 * kOperand);
+              tma_3d_pair(there, &map_y, o0, i * kTok, term, bar_y);
+              tma_3d_pair(there + kHalf, &map_y, o0 + 64, i * kTok, term, bar_y);
+            }
           }
         }
       }
@@ -268,7 +273,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GradWarps<kExact>::k
         q.drain(ints, kWaitLimit);
         if (rank == 0) y.drain(full, kWaitLimit);
       }
-    } else if (warp == W::kIssue && lane == 0 && rank == 0) {
+    } else if (warp == W::kIssue && rank == 0) {
+      const bool elected = elect_one();
       Ring<kXStages> x;
       Ring<kYStages> y;
       Ring<2> out;
@@ -276,28 +282,30 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GradWarps<kExact>::k
         const int part = w / tiles;
         const int count = min(g.pieces, (part + 1) * g.per) - part * g.per;
         for (int i = 0; i < count && ok; out.next()) {
-          ok = out.wait_empty(freed, kWaitLimit);
+          ok = __all_sync(0xffffffffu, out.wait_empty(freed, kWaitLimit));
           if (!ok) break;
           tcgen05_after_sync();
           const int end = min(count, i + g.chunk);
           for (bool add = false; i < end && ok; ++i, x.next()) {
-            ok = x.wait_full(ready, kWaitLimit);
+            ok = __all_sync(0xffffffffu, x.wait_full(ready, kWaitLimit));
             const uint64_t da = smem_desc(xs + x.stage * kOperand, kHalf, 1024);
             for (int term = 0; term < g.terms && ok; ++term, y.next()) {
-              ok = y.wait_full(full, kWaitLimit);
+              ok = __all_sync(0xffffffffu, y.wait_full(full, kWaitLimit));
               if (!ok) break;
               tcgen05_after_sync();
               const uint64_t db = smem_desc(ys + y.stage * kOperand, kHalf, 1024);
+              if (elected) {
 #pragma unroll
-              for (int j = 0; j < kTok / 16; ++j) {  // 16 tokens per MMA: 16 rows of 128 bytes
-                mma_bf16<2>(acc + out.stage * 256, da + j * (2048 >> 4), db + j * (2048 >> 4), idesc_bf16_mn(256, 256), add);
-                add = true;
+                for (int j = 0; j < kTok / 16; ++j)  // 16 tokens per MMA: 16 rows of 128 bytes
+                  mma_bf16<2>(acc + out.stage * 256, da + j * (2048 >> 4), db + j * (2048 >> 4), idesc_bf16_mn(256, 256),
+                              add || j > 0);
+                mma_commit<2>(y_empty + 8 * y.stage);
               }
-              mma_commit<2>(y_empty + 8 * y.stage);
+              add = true;
             }
-            mma_commit<2>(x_empty + 8 * x.stage);
+            if (elected) mma_commit<2>(x_empty + 8 * x.stage);
           }
-          mma_commit<2>(done + 8 * out.stage);
+          if (elected) mma_commit<2>(done + 8 * out.stage);
         }
       }
     } else if (warp >= W::kConvert0) {

@@ -193,7 +193,7 @@ __global__ void __launch_bounds__(192, 2)
   __shared__ uint32_t tmem_slot;
   const uint32_t tiles = (smem_addr(smem_raw) + 1023) & ~1023u;
   const uint32_t full = smem_addr(bars), empty = full + 8 * Cfg::kStages, done = empty + 8 * Cfg::kStages;
-  const int warp = warp_id(), lane = lane_id();
+  const int warp = __shfl_sync(0xffffffffu, warp_id(), 0), lane = lane_id();
   const int tile = static_cast<int>(blockIdx.x) / split;
   const int part = static_cast<int>(blockIdx.x) % split;
   const int channel0 = (tile % channel_tiles) * 128;
@@ -216,38 +216,40 @@ __global__ void __launch_bounds__(192, 2)
   tcgen05_before_sync();
   __syncthreads();
   tcgen05_after_sync();
-  const uint32_t acc = tmem_slot;
+  const uint32_t acc = __shfl_sync(0xffffffffu, tmem_slot, 0);
   bool ok = true;
 
   if (warp == 4) {
-    if (lane == 0) {
-      Ring<Cfg::kStages> at;
-      for (int i = 0; i < count; ++i, at.next()) {
-        ok = at.wait_empty(empty, kWaitLimit);
-        if (!ok) break;
-        const uint32_t a = tiles + at.stage * (Cfg::kA + Cfg::kB), bar = full + 8 * at.stage;
+    const bool elected = elect_one();
+    Ring<Cfg::kStages> at;
+    for (int i = 0; i < count; ++i, at.next()) {
+      ok = __all_sync(0xffffffffu, at.wait_empty(empty, kWaitLimit));
+      if (!ok) break;
+      const uint32_t a = tiles + at.stage * (Cfg::kA + Cfg::kB), bar = full + 8 * at.stage;
+      if (elected) {
         mbar_expect_tx(bar, Cfg::kA + Cfg::kB);
         tma_2d(a, &map_w, (first + i) * kPieceK, channel0, bar);
         tma_2d(a + Cfg::kA, &map_x, (first + i) * kPieceK, token0, bar);
       }
-      if (!ok) at.drain(full, kWaitLimit);  // before the memory is given back
     }
+    if (!ok) at.drain(full, kWaitLimit);  // before the memory is given back
   } else if (warp == 5) {
-    if (lane == 0) {
-      Ring<Cfg::kStages> at;
-      for (int i = 0; i < count; ++i, at.next()) {
-        ok = at.wait_full(full, kWaitLimit);
-        if (!ok) break;
-        tcgen05_after_sync();
-        const uint32_t a = tiles + at.stage * (Cfg::kA + Cfg::kB);
-        const uint64_t da = smem_desc(a, 16, 1024), db = smem_desc(a + Cfg::kA, 16, 1024);
+    const bool elected = elect_one();
+    Ring<Cfg::kStages> at;
+    for (int i = 0; i < count; ++i, at.next()) {
+      ok = __all_sync(0xffffffffu, at.wait_full(full, kWaitLimit));
+      if (!ok) break;
+      tcgen05_after_sync();
+      const uint32_t a = tiles + at.stage * (Cfg::kA + Cfg::kB);
+      const uint64_t da = smem_desc(a, 16, 1024), db = smem_desc(a + Cfg::kA, 16, 1024);
+      if (elected) {
 #pragma unroll
         for (int j = 0; j < kPieceK / kStepK; ++j)
           mma_i8<1>(acc, da + j * (kStepK >> 4), db + j * (kStepK >> 4), idesc_i8(128, kTok), i > 0 || j > 0);
         mma_commit<1>(empty + 8 * at.stage);
       }
-      mma_commit<1>(done);
     }
+    if (elected) mma_commit<1>(done);
   } else {
     ok = mbar_wait_bounded(done, 0, kWaitLimit);
     tcgen05_after_sync();
@@ -358,7 +360,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(192, 1)
   const uint32_t tiles = (smem_addr(smem_raw) + 1023) & ~1023u;
   const uint32_t full = smem_addr(bars), empty = full + 8 * kPairStages;
   const uint32_t done = empty + 8 * kPairStages, freed = done + 16;  // per accumulator buffer
-  const int warp = warp_id(), lane = lane_id();
+  const int warp = __shfl_sync(0xffffffffu, warp_id(), 0), lane = lane_id();
   const int rank = static_cast<int>(cluster_rank());
   const int pair = static_cast<int>(blockIdx.x) >> 1, pairs = static_cast<int>(gridDim.x) >> 1;
   const int all = channel_tiles * token_tiles;
@@ -380,47 +382,52 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(192, 1)
   tcgen05_before_sync();
   cluster_sync_all();
   tcgen05_after_sync();
-  const uint32_t acc = tmem_slot;
+  const uint32_t acc = __shfl_sync(0xffffffffu, tmem_slot, 0);
   bool ok = true;
 
   if (warp == 4) {
-    if (lane == 0) {
-      const uint32_t full0 = map_shared(full, 0);
-      Ring<kPairStages> at;
-      for (int t = pair; t < all && ok; t += pairs) {
-        const TileAt tile = tile_at(t, channel_tiles, token_tiles);
-        const int c0 = tile.channel * 256 + rank * 128, t0 = tile.token * 256 + rank * 128;
-        for (int i = 0; i < p.pieces; ++i, at.next()) {
-          ok = at.wait_empty(empty, kWaitLimit);
-          if (!ok) break;
-          const uint32_t a = tiles + at.stage * kPairStage, bar = full0 + 8 * at.stage;
+    const bool elected = elect_one();
+    const uint32_t full0 = map_shared(full, 0);
+    Ring<kPairStages> at;
+    for (int t = pair; t < all && ok; t += pairs) {
+      const TileAt tile = tile_at(t, channel_tiles, token_tiles);
+      const int c0 = tile.channel * 256 + rank * 128, t0 = tile.token * 256 + rank * 128;
+      for (int i = 0; i < p.pieces; ++i, at.next()) {
+        ok = __all_sync(0xffffffffu, at.wait_empty(empty, kWaitLimit));
+        if (!ok) break;
+        const uint32_t a = tiles + at.stage * kPairStage, bar = full0 + 8 * at.stage;
+        if (elected) {
           if (rank == 0) mbar_expect_tx(full + 8 * at.stage, 2 * kPairStage);
           tma_2d_pair(a, &map_w, i * kPieceK, c0, bar);
           tma_2d_pair(a + 128 * kPieceK, &map_x, i * kPieceK, t0, bar);
         }
       }
-      if (!ok && rank == 0) at.drain(full, kWaitLimit);
     }
+    if (!ok && rank == 0) at.drain(full, kWaitLimit);
   } else if (warp == 5) {
-    if (lane == 0 && rank == 0) {
+    if (rank == 0) {
+      const bool elected = elect_one();
       Ring<kPairStages> at;
       Ring<2> out;
       for (int t = pair; t < all && ok; t += pairs, out.next()) {
-        ok = out.wait_empty(freed, kWaitLimit);
+        ok = __all_sync(0xffffffffu, out.wait_empty(freed, kWaitLimit));
         if (!ok) break;
         tcgen05_after_sync();
         for (int i = 0; i < p.pieces; ++i, at.next()) {
-          ok = at.wait_full(full, kWaitLimit);
+          ok = __all_sync(0xffffffffu, at.wait_full(full, kWaitLimit));
           if (!ok) break;
           tcgen05_after_sync();
           const uint32_t a = tiles + at.stage * kPairStage;
           const uint64_t da = smem_desc(a, 16, 1024), db = smem_desc(a + 128 * kPieceK, 16, 1024);
+          if (elected) {
 #pragma unroll
-          for (int j = 0; j < kPieceK / kStepK; ++j)
-            mma_i8<2>(acc + out.stage * 256, da + j * (kStepK >> 4), db + j * (kStepK >> 4), idesc_i8(256, 256), i > 0 || j > 0);
-          mma_commit<2>(empty + 8 * at.stage);
+            for (int j = 0; j < kPieceK / kStepK; ++j)
+              mma_i8<2>(acc + out.stage * 256, da + j * (kStepK >> 4), db + j * (kStepK >> 4), idesc_i8(256, 256),
+                        i > 0 || j > 0);
+            mma_commit<2>(empty + 8 * at.stage);
+          }
         }
-        mma_commit<2>(done + 8 * out.stage);
+        if (elected) mma_commit<2>(done + 8 * out.stage);
       }
     }
   } else {

@@ -56,6 +56,16 @@ inline bool make_map(CUtensorMap* map, CUtensorMapDataType type, int rank, const
 
 // ---- device: clusters and barriers -----------------------------------------------
 
+// One thread of a converged warp. Roles of one thread run as whole warps in which only
+// the copies, MMAs and commits are the elected thread's: their operands then stay in
+// uniform registers. (With the loop itself inside a branch of one lane, issuing the
+// four MMAs of a stage took about 450 clocks, of the 512 that they run.)
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+  return p != 0;
+}
+
 __device__ __forceinline__ uint32_t cluster_rank() {
   uint32_t r;
   asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
