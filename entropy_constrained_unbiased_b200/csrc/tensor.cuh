@@ -88,8 +88,12 @@ __device__ __forceinline__ int ld_shared_cluster(uint32_t addr) {
 __device__ __forceinline__ void mbar_arrive(uint32_t mbar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(mbar) : "memory");
 }
+// On a barrier of either CTA of the cluster. What is handed over lies in this CTA's
+// shared or tensor memory and was ordered before by a proxy or tcgen05 fence, so the
+// arrival needs no release at cluster scope (which took 2000 clocks per stage of the
+// converters, waiting for all earlier stores).
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t mbar) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(mbar) : "memory");
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(mbar) : "memory");
 }
 
 // A place in a ring of kStages stages, walked in order: the stage, the parity of the
