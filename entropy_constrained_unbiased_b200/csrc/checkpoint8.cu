@@ -25,47 +25,79 @@ __device__ __forceinline__ uint32_t scale_byte(uint32_t a_bits) {
   return b > 248 ? kScaleNaN : static_cast<uint32_t>(b < 1 ? 1 : b);
 }
 
+// Four bytes, each filled with the sign bit of the byte that its selector nibble (8 plus
+// the byte's number) names.
+__device__ __forceinline__ uint32_t byte_signs(uint32_t a, uint32_t b, uint32_t selector) {
+  uint32_t r;
+  asm("prmt.b32 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(selector));
+  return r;
+}
+
 // One thread per 8 entries (one Philox block), four threads per block of 32; a CTA
-// covers blockDim.y rows by 8 * blockDim.x columns.
-template <int kType>
+// covers blockDim.y rows by 8 * blockDim.x columns. Bound by instruction issue: the
+// ten Philox rounds are half of the work.
+//
+// With Z = nearest(2^16 |x| / s), the magnitude floor(|x| / s) plus one if 16 random
+// bits u are below the fraction's nearest(65536 f) is (Z + 65535 - u) >> 16. Adding
+// 2^23 in a fused multiply-add leaves Z in the low 23 bits (the scaling is exact, so
+// there is one rounding, ties to even), and the magnitude in bits 16 to 22 of the sum.
+template <int kType, bool kSeedWord>
 __global__ void __launch_bounds__(256)
     k_checkpoint8(const typename Elem<kType>::T* __restrict__ X, int64_t t, int64_t k, int64_t ldx, bool wide,
-                  uint64_t seed, const uint64_t* __restrict__ seed_add, int8_t* __restrict__ Q, int64_t ldq,
-                  uint8_t* __restrict__ S, int64_t lds) {
+                  const Philox4x32::RoundKeys keys, uint64_t seed, const uint64_t* __restrict__ seed_add,
+                  int8_t* __restrict__ Q, int64_t ldq, uint8_t* __restrict__ S, int64_t lds) {
   const int64_t r = static_cast<int64_t>(blockIdx.x) * blockDim.y + threadIdx.y;
   const int64_t c = static_cast<int64_t>(blockIdx.y) * blockDim.x + threadIdx.x;
   const int64_t pieces = (k + 31) / 32 * 4;
-  if (seed_add) seed += *seed_add;
-  float v[8];
   const bool live = r < t && c < pieces;
-  if (live)
-    load8<kType>(X + r * ldx, c * 8, k, wide, v);
-  else
-#pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = 0.0f;
-  uint32_t m = 0;
-#pragma unroll
-  for (int e = 0; e < 8; ++e) m = max(m, __float_as_uint(v[e]) & 0x7fffffffu);
+  Eight<kType> in = {};
+  if (live) in = load8<kType>(X + r * ldx, c * 8, k, wide);
+  Largest<kType> top;
+  top.add(in);
+  uint32_t m = top.bits();
+  // the random bits do not wait for the load
+  const uint4 counter = make_uint4(static_cast<uint32_t>(c), static_cast<uint32_t>(r), kStreamCheckpoint, 0);
+  uint4 u;
+  if constexpr (kSeedWord) {
+    const uint64_t key = seed + *seed_add;
+    u = Philox4x32::block(counter, static_cast<uint32_t>(key), static_cast<uint32_t>(key >> 32));
+  } else {
+    u = Philox4x32::block(counter, keys);
+  }
   m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
   m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
   if (!live) return;
   const uint32_t b = scale_byte(m);
   uint32_t word[2] = {0, 0};
-  if (b != kScaleNaN && m != 0) {
-    const uint4 u = Philox4x32::block(
-        make_uint4(static_cast<uint32_t>(c), static_cast<uint32_t>(r), kStreamCheckpoint, 0),
-        static_cast<uint32_t>(seed), static_cast<uint32_t>(seed >> 32));
-    const uint32_t rnd[4] = {u.x, u.y, u.z, u.w};
-    const float inv = __uint_as_float((254u - b) << 23);  // 1 / s, exact
+  if (b != kScaleNaN) {
+    const uint32_t rnd[4] = {~u.x, ~u.y, ~u.z, ~u.w};  // 65535 - u in either half
+    const float up = __uint_as_float((254u - b) << 23) * 65536.0f;  // 2^16 / s, exact: b >= 17, or
+    const float inv = __uint_as_float((254u - b) << 23);            // in two steps for smaller s
+    const bool small = b < 17;
+    float v[8];
+    floats8<kType>(in, v);
+    const uint32_t* raw = reinterpret_cast<const uint32_t*>(&in);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const float z = fabsf(v[e]) * inv;
-      const float low = floorf(z);
-      const int up = __float2int_rn((z - low) * 65536.0f);
-      const int u16 = static_cast<int>((e & 1) ? rnd[e >> 1] >> 16 : rnd[e >> 1] & 0xffffu);
-      int q = static_cast<int>(low) + (u16 < up ? 1 : 0);
-      q = v[e] < 0.0f ? -q : q;
-      word[e >> 2] |= (static_cast<uint32_t>(q) & 0xffu) << (8 * (e & 3));
+    for (int h = 0; h < 2; ++h) {
+      uint32_t q[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float x = fabsf(v[4 * h + e]);
+        const float z = small ? fmaf(x * inv, 65536.0f, 8388608.0f) : fmaf(x, up, 8388608.0f);
+        const uint32_t w = rnd[2 * h + (e >> 1)];
+        q[e] = __float_as_uint(z) + ((e & 1) ? w >> 16 : w & 0xffffu);
+      }
+      // the magnitudes (byte 2 of each sum), negated where the sign byte is all ones; the
+      // addition of one stays inside its byte
+      const uint32_t mag = __byte_perm(__byte_perm(q[0], q[1], 0x0062), __byte_perm(q[2], q[3], 0x0062), 0x5410);
+      uint32_t neg;
+      if constexpr (kType == kF32)
+        neg = __byte_perm(byte_signs(raw[4 * h], raw[4 * h + 1], 0x00FB),
+                          byte_signs(raw[4 * h + 2], raw[4 * h + 3], 0x00FB), 0x5410);
+      else
+        neg = byte_signs(raw[2 * h], raw[2 * h + 1], 0xFDB9);
+      const uint32_t flip = mag ^ neg, one = neg & 0x01010101u;
+      word[h] = ((flip & 0x7f7f7f7fu) + one) ^ (flip & 0x80808080u);
     }
   }
   *reinterpret_cast<uint2*>(Q + r * ldq + c * 8) = make_uint2(word[0], word[1]);
@@ -76,23 +108,45 @@ __device__ __forceinline__ float scale_value(uint32_t b) {
   return __uint_as_float(b == kScaleNaN ? 0x7fc00000u : b << 23);
 }
 
+// One thread per 8 entries. Rows off the 16-byte boundary go through shared memory, so
+// that a warp's stores of single entries are adjacent (a thread's own eight at a time
+// took 10.3 instead of 5 us for 3001 x 777 float32).
 template <int kType>
 __global__ void __launch_bounds__(256)
     k_checkpoint8_restore(const int8_t* __restrict__ Q, int64_t ldq, const uint8_t* __restrict__ S, int64_t lds,
                           int64_t t, int64_t k, typename Elem<kType>::T* __restrict__ X, int64_t ldx, bool wide) {
+  __shared__ float lines[8][8 * 33];
   const int64_t r = static_cast<int64_t>(blockIdx.x) * blockDim.y + threadIdx.y;
   const int64_t c = static_cast<int64_t>(blockIdx.y) * blockDim.x + threadIdx.x;
-  if (r >= t || c * 8 >= k) return;
-  const uint2 w = __ldg(reinterpret_cast<const uint2*>(Q + r * ldq + c * 8));
-  const float s = scale_value(S[r * lds + (c >> 2)]);
-  float v[8];
+  const bool live = r < t && c * 8 < k;
+  float v[8] = {};
+  if (live) {
+    const uint2 w = __ldg(reinterpret_cast<const uint2*>(Q + r * ldq + c * 8));
+    const float s = scale_value(S[r * lds + (c >> 2)]);
 #pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    const uint32_t x = e < 4 ? w.x : w.y;
-    v[e] = static_cast<float>(static_cast<int8_t>(x >> (8 * (e & 3)))) * s;
-    if (kType == kF16 && fabsf(v[e]) > 65504.0f) v[e] = copysignf(65504.0f, v[e]);
+    for (int e = 0; e < 8; ++e) {
+      const uint32_t x = e < 4 ? w.x : w.y;
+      v[e] = static_cast<float>(static_cast<int8_t>(x >> (8 * (e & 3)))) * s;
+      if (kType == kF16 && fabsf(v[e]) > 65504.0f) v[e] = copysignf(65504.0f, v[e]);
+    }
   }
-  store8<kType>(X + r * ldx, c * 8, k, wide, v);
+  if (wide || blockDim.x < 32) {
+    if (live) store8<kType>(X + r * ldx, c * 8, k, wide, v);
+    return;
+  }
+  const int lane = lane_id();  // a warp's pieces are adjacent pieces of one row
+  float* line = lines[(threadIdx.y * blockDim.x + threadIdx.x) >> 5];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) line[lane * 8 + e + (lane >> 2)] = v[e];
+  __syncwarp();
+  const int64_t c0 = (c - lane) * 8;
+  if (r < t) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const int64_t j = c0 + e * 32 + lane;
+      if (j < k) X[r * ldx + j] = Elem<kType>::put(line[e * 32 + lane + e]);
+    }
+  }
 }
 
 // Threads along a row and rows per CTA (256 threads), and the grid, for `pieces`
@@ -136,7 +190,8 @@ constexpr int kQStage = kInts + kScales;
 constexpr int kQStages = 7, kXStages = 4, kYStages = 6;
 constexpr int kGradSmem = kQStages * kQStage + kXStages * kOperand + kYStages * kOperand + 1024;
 
-// Warps: the epilogue's, the producer, the MMA issuer, the converters. The converters
+// Warps: the epilogue's, the producers of dY and of the integers, the MMA issuer, the
+// converters. The converters
 // come in kXStages groups that take the stages in turn, so that the latencies of one
 // stage's conversion (its wait, its loads, the fence, the arrival at the other CTA)
 // are covered by three others'. kExact holds 128 sums a thread in the epilogue's
@@ -145,9 +200,9 @@ constexpr int kGradSmem = kQStages * kQStage + kXStages * kOperand + kYStages * 
 template <bool kExact>
 struct GradWarps {
   static constexpr int kEpilogue = kExact ? 8 : 4;
-  static constexpr int kLoad = kEpilogue, kIssue = kEpilogue + 1;
-  static constexpr int kConvert0 = kExact ? 12 : 6;
-  static constexpr int kConvert = kExact ? 4 : 8;
+  static constexpr int kLoad = kEpilogue, kIssue = kEpilogue + 1, kLoadInts = kEpilogue + 2;
+  static constexpr int kConvert0 = kExact ? 12 : 7;
+  static constexpr int kConvert = kExact ? 4 : 16;
   static constexpr int kThreads = 32 * (kConvert0 + kConvert);
 };
 
@@ -242,13 +297,32 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GradWarps<kExact>::k
     if (warp == W::kLoad) {
       const bool elected = elect_one();
       const uint32_t full0 = map_shared(full, 0);
-      Ring<kQStages> q;
       Ring<kYStages> y;
       for (int w = pair; w < all && ok; w += pairs) {
         const int tile = w % tiles, part = w / tiles;
-        const int f0 = (tile % g.feature_tiles) * 256 + rank * 128, o0 = (tile / g.feature_tiles) * 256 + rank * 128;
+        const int o0 = (tile / g.feature_tiles) * 256 + rank * 128;
         const int last = min(g.pieces, (part + 1) * g.per);
-        for (int i = part * g.per; i < last && ok; ++i, q.next()) {
+        for (int i = part * g.per; i < last && ok; ++i)
+          for (int term = 0; term < g.terms; ++term, y.next()) {
+            ok = __all_sync(0xffffffffu, y.wait_empty(y_empty, kWaitLimit));
+            if (!ok) break;
+            const uint32_t to = ys + y.stage * kOperand, bar = full0 + 8 * y.stage;
+            if (elected) {
+              if (rank == 0) mbar_expect_tx(full + 8 * y.stage, 2 * kOperand);
+              tma_3d_pair(to, &map_y, o0, i * kTok, term, bar);
+              tma_3d_pair(to + kHalf, &map_y, o0 + 64, i * kTok, term, bar);
+            }
+          }
+      }
+      if (!ok && rank == 0) y.drain(full, kWaitLimit);  // before the memory is given back
+    } else if (warp == W::kLoadInts) {
+      const bool elected = elect_one();
+      Ring<kQStages> q;
+      for (int w = pair; w < all && ok; w += pairs) {
+        const int tile = w % tiles, part = w / tiles;
+        const int f0 = (tile % g.feature_tiles) * 256 + rank * 128;
+        const int last = min(g.pieces, (part + 1) * g.per);
+        for (int i = part * g.per; i < last; ++i, q.next()) {
           ok = __all_sync(0xffffffffu, q.wait_empty(q_empty, kWaitLimit));
           if (!ok) break;
           const uint32_t to = qs + q.stage * kQStage, bar = ints + 8 * q.stage;
@@ -257,22 +331,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GradWarps<kExact>::k
             tma_2d(to, &map_q, f0, i * kTok, bar);
             tma_2d(to + kInts, &map_s, (f0 / 32) & ~15, i * kTok, bar);
           }
-          for (int term = 0; term < g.terms; ++term, y.next()) {
-            ok = __all_sync(0xffffffffu, y.wait_empty(y_empty, kWaitLimit));
-            if (!ok) break;
-            const uint32_t there = ys + y.stage * kOperand, bar_y = full0 + 8 * y.stage;
-            if (elected) {
-              if (rank == 0) mbar_expect_tx(full + 8 * y.stage, 2 * kOperand);
-              tma_3d_pair(there, &map_y, o0, i * kTok, term, bar_y);
-              tma_3d_pair(there + kHalf, &map_y, o0 + 64, i * kTok, term, bar_y);
-            }
-          }
         }
       }
-      if (!ok) {  // before the memory is given back
-        q.drain(ints, kWaitLimit);
-        if (rank == 0) y.drain(full, kWaitLimit);
-      }
+      if (!ok) q.drain(ints, kWaitLimit);
     } else if (warp == W::kIssue && rank == 0) {
       const bool elected = elect_one();
       Ring<kXStages> x;
@@ -437,7 +498,7 @@ __global__ void __launch_bounds__(256)
   const int64_t c = static_cast<int64_t>(blockIdx.y) * blockDim.x + threadIdx.x;
   if (r >= t || c * 8 >= o) return;
   float v[8];
-  load8<kIn>(dY + r * ldy, c * 8, o, wide, v);
+  floats8<kIn>(load8<kIn>(dY + r * ldy, c * 8, o, wide), v);
 #pragma unroll
   for (int term = 0; term < kTerms; ++term) {
     uint32_t w[8];
@@ -462,7 +523,9 @@ __global__ void __launch_bounds__(256)
   const int64_t c = static_cast<int64_t>(blockIdx.y) * 256 + threadIdx.x, r = blockIdx.x;
   if (c >= k) return;
   float sum = 0.0f;
-  for (int i = 0; i < split; ++i) sum += part[(i * o + r) * k + c];
+  const float* from = part + r * k + c;
+#pragma unroll 8
+  for (int i = 0; i < split; ++i) sum += __ldg(from + i * (o * k));
   dW[r * ldw + c] = Elem<kOut>::put(sum);
 }
 
@@ -548,15 +611,20 @@ cudaError_t launch_checkpoint8(const void* X, int type, int64_t t, int64_t k, in
   dim3 grid, block;
   piece_grid(t, (k + 31) / 32 * 4, &grid, &block);
   const bool wide = rows_aligned16(X, ldx, type_bytes(type));
-  if (type == kF32)
-    k_checkpoint8<kF32><<<grid, block, 0, st>>>(static_cast<const float*>(X), t, k, ldx, wide, seed, seed_add, q, ldq,
-                                                scale, lds);
-  else if (type == kBF16)
-    k_checkpoint8<kBF16><<<grid, block, 0, st>>>(static_cast<const __nv_bfloat16*>(X), t, k, ldx, wide, seed, seed_add,
-                                                 q, ldq, scale, lds);
-  else
-    k_checkpoint8<kF16><<<grid, block, 0, st>>>(static_cast<const __half*>(X), t, k, ldx, wide, seed, seed_add, q, ldq,
-                                                scale, lds);
+  const Philox4x32::RoundKeys keys = Philox4x32::round_keys(static_cast<uint32_t>(seed), static_cast<uint32_t>(seed >> 32));
+  const auto run = [&](auto kernel, const auto* x) {
+    kernel<<<grid, block, 0, st>>>(x, t, k, ldx, wide, keys, seed, seed_add, q, ldq, scale, lds);
+  };
+  if (type == kF32) {
+    const auto* x = static_cast<const float*>(X);
+    seed_add ? run(k_checkpoint8<kF32, true>, x) : run(k_checkpoint8<kF32, false>, x);
+  } else if (type == kBF16) {
+    const auto* x = static_cast<const __nv_bfloat16*>(X);
+    seed_add ? run(k_checkpoint8<kBF16, true>, x) : run(k_checkpoint8<kBF16, false>, x);
+  } else {
+    const auto* x = static_cast<const __half*>(X);
+    seed_add ? run(k_checkpoint8<kF16, true>, x) : run(k_checkpoint8<kF16, false>, x);
+  }
   note_launch();
   return cudaGetLastError();
 }

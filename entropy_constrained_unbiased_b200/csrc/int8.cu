@@ -17,23 +17,11 @@ namespace {
 // ---- quantiser -------------------------------------------------------------------
 //
 // Two steps per row, a = max |x| and q = nearest(127 x / a). A row's kTPR threads
-// keep it in registers between the two (kKeep pieces of 8 entries each), so X is
-// read once; longer rows read the rest again, from L2.
+// keep it in registers between the two (kKeep pieces of 8 entries each, as they lie in
+// memory), so X is read once; longer rows read the rest again, from L2. Bound by
+// memory: 3 bytes for a bfloat16 entry leave about 16 instructions for it.
 
-// nearest(127 x / a) with ties to even, decided by the exact quotient: the float32
-// product t is within 127 * 2^-22 of it, so only a t that close to a half needs
-// the fp64 quotient (127 x is exact there, and a quotient of a 31-bit by a 24-bit
-// integer that is not a half differs from it by more than an fp64 rounding).
-__device__ __forceinline__ int nearest127(float x, float xs, float r, float a) {
-  const float t = xs * r;
-  int q = __float2int_rn(t);
-  if (fabsf(t - static_cast<float>(q)) > 0.5f - 0x1p-14f)
-    q = __double2int_rn(__ddiv_rn(static_cast<double>(x) * 127.0, static_cast<double>(a)));
-  return q;
-}
-
-// A row's quantisation from its largest magnitude, given as bits (NaN and infinity
-// order above every finite value).
+// A row's quantisation from its largest magnitude, given as the bits of a float.
 struct RowScale {
   float a, lift, inv, scale;
   bool bad;
@@ -48,15 +36,37 @@ __device__ __forceinline__ RowScale row_scale(uint32_t a_bits) {
   s.scale = s.bad ? __uint_as_float(0x7fc00000u) : __fdiv_rn(s.a, 127.0f);
   return s;
 }
-// Eight integers of a row, in order.
+// Eight integers of a row, in order: nearest(127 x / a) with ties to even, decided by
+// the exact quotient. The float32 product t is within 127 * 2^-23 < 2^-16 of it, so
+// only a t that close to a half needs the fp64 quotient (127 x is exact there, and a
+// quotient of a 31-bit by a 24-bit integer that is not a half differs from it by more
+// than an fp64 rounding). Adding 1.5 * 2^23 leaves the nearest integer in the low
+// bits, two's complement.
 __device__ __forceinline__ uint2 quantize8(const float (&v)[8], const RowScale& s) {
-  uint32_t word[2] = {0, 0};
-  if (s.inv != 0.0f) {
+  if (s.inv == 0.0f) return make_uint2(0, 0);
+  constexpr float kInt = 12582912.0f;
+  uint32_t b[8];
+  float far = 0.0f;
 #pragma unroll
-    for (int e = 0; e < 8; ++e)
-      word[e >> 2] |= (static_cast<uint32_t>(nearest127(v[e], v[e] * s.lift, s.inv, s.a)) & 0xffu) << (8 * (e & 3));
+  for (int e = 0; e < 8; ++e) {
+    const float t = __fmul_rn(v[e] * s.lift, s.inv), m = __fadd_rn(t, kInt);
+    far = fmaxf(far, fabsf(t - __fadd_rn(m, -kInt)));
+    b[e] = __float_as_uint(m);
   }
-  return make_uint2(word[0], word[1]);
+  if (far > 0.5f - 0x1p-16f) {
+#pragma unroll 1
+    for (int e = 0; e < 8; ++e) {
+      float x = v[0];
+#pragma unroll
+      for (int i = 1; i < 8; ++i) x = e == i ? v[i] : x;
+      const uint32_t q = static_cast<uint32_t>(
+          __double2int_rn(__ddiv_rn(static_cast<double>(x) * 127.0, static_cast<double>(s.a))));
+#pragma unroll
+      for (int i = 0; i < 8; ++i) b[i] = e == i ? q : b[i];
+    }
+  }
+  return make_uint2(__byte_perm(__byte_perm(b[0], b[1], 0x0040), __byte_perm(b[2], b[3], 0x0040), 0x5410),
+                    __byte_perm(__byte_perm(b[4], b[5], 0x0040), __byte_perm(b[6], b[7], 0x0040), 0x5410));
 }
 
 template <int kType, int kTPR, int kKeep, bool kLong>
@@ -70,28 +80,22 @@ __global__ void __launch_bounds__(kTPR < 128 ? 128 : kTPR)
   const int64_t r = static_cast<int64_t>(blockIdx.x) * kRows + threadIdx.x / kTPR;
   const bool live = r < n;
   const auto* row = X + (live ? r : 0) * ldx;
-  float v[kKeep][8];
-  uint32_t m = 0;  // max |x| as bits: NaN and infinity order above every finite value
+  Eight<kType> v[kKeep];
+  Largest<kType> top;
 #pragma unroll
-  for (int i = 0; i < kKeep; ++i) {
-    load8<kType>(row, static_cast<int64_t>(lane + i * kTPR) * 8, k, wide, v[i]);
+  for (int i = 0; i < kKeep; ++i) v[i] = load8<kType>(row, static_cast<int64_t>(lane + i * kTPR) * 8, k, wide);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) m = max(m, __float_as_uint(v[i][e]) & 0x7fffffffu);
-  }
+  for (int i = 0; i < kKeep; ++i) top.add(v[i]);
   if (kLong) {
-    for (int64_t j = static_cast<int64_t>(lane + kKeep * kTPR) * 8; j < k; j += kTPR * 8) {
-      float w[8];
-      load8<kType>(row, j, k, wide, w);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) m = max(m, __float_as_uint(w[e]) & 0x7fffffffu);
-    }
+#pragma unroll 4
+    for (int64_t j = static_cast<int64_t>(lane + kKeep * kTPR) * 8; j < k; j += kTPR * 8)
+      top.add(load8<kType>(row, j, k, wide));
   }
-  m = __reduce_max_sync(0xffffffffu, m);
+  uint32_t m = __reduce_max_sync(0xffffffffu, top.bits());
   if (kTPR > 32) {
     if (lane_id() == 0) part[warp_id()] = m;
     __syncthreads();
-    m = part[lane_id() % (kTPR / 32)];
-    m = __reduce_max_sync(0xffffffffu, m);
+    m = __reduce_max_sync(0xffffffffu, part[lane_id() % (kTPR / 32)]);
   }
   if (!live) return;
   const RowScale a = row_scale(m);
@@ -100,23 +104,22 @@ __global__ void __launch_bounds__(kTPR < 128 ? 128 : kTPR)
     status[r] = a.bad ? kStatusRange : kStatusOk;
   }
   int8_t* out = Q + r * ldq;
-  const auto put = [&](int64_t j, const float(&w)[8]) {
+  const auto put = [&](int64_t j, const Eight<kType>& e) {
     if (j >= k) return;
+    float w[8];
+    floats8<kType>(e, w);
     const uint2 q = quantize8(w, a);
     if (j + 8 <= k) {
       *reinterpret_cast<uint2*>(out + j) = q;
     } else {
-      for (int e = 0; j + e < k; ++e) out[j + e] = static_cast<int8_t>((e < 4 ? q.x : q.y) >> (8 * (e & 3)));
+      for (int i = 0; j + i < k; ++i) out[j + i] = static_cast<int8_t>((i < 4 ? q.x : q.y) >> (8 * (i & 3)));
     }
   };
 #pragma unroll
   for (int i = 0; i < kKeep; ++i) put(static_cast<int64_t>(lane + i * kTPR) * 8, v[i]);
   if (kLong) {
-    for (int64_t j = static_cast<int64_t>(lane + kKeep * kTPR) * 8; j < k; j += kTPR * 8) {
-      float w[8];
-      load8<kType>(row, j, k, wide, w);
-      put(j, w);
-    }
+    for (int64_t j = static_cast<int64_t>(lane + kKeep * kTPR) * 8; j < k; j += kTPR * 8)
+      put(j, load8<kType>(row, j, k, wide));
   }
 }
 
@@ -125,13 +128,15 @@ cudaError_t int8_rows(const void* X, int64_t n, int64_t k, int64_t ldx, int8_t* 
                       int32_t* status, cudaStream_t st) {
   const auto* x = static_cast<const typename Elem<kType>::T*>(X);
   const bool wide = rows_aligned16(X, ldx, type_bytes(kType));
+  constexpr int kMost = kType == kF32 ? 4 : 8;  // 16384 16-bit or 8192 32-bit entries in registers
+  // a warp, four or eight of them per row; few rows take the most threads (latency)
   if (k <= 1024 && n > 148) {
     k_int8_rows<kType, 32, 4, false>
         <<<static_cast<unsigned>((n + 3) / 4), 128, 0, st>>>(x, n, k, ldx, wide, Q, ldq, scale, status);
-  } else if (k <= 4096) {
+  } else if (k <= 4096 && n > 148) {
     k_int8_rows<kType, 128, 4, false><<<static_cast<unsigned>(n), 128, 0, st>>>(x, n, k, ldx, wide, Q, ldq, scale, status);
   } else {
-    k_int8_rows<kType, 512, 4, true><<<static_cast<unsigned>(n), 512, 0, st>>>(x, n, k, ldx, wide, Q, ldq, scale, status);
+    k_int8_rows<kType, 256, kMost, true><<<static_cast<unsigned>(n), 256, 0, st>>>(x, n, k, ldx, wide, Q, ldq, scale, status);
   }
   note_launch();
   return cudaGetLastError();
@@ -511,7 +516,7 @@ __global__ void __launch_bounds__(kFewThreads)
     k_int8_few(const void* __restrict__ X, int64_t ldx, bool wide, const int8_t* __restrict__ B, int64_t ldb,
                const Product p, int64_t k) {
   extern __shared__ int4 tokens[];  // [m][kp / 16]
-  __shared__ uint32_t part[kFewThreads / 32][kM];
+  __shared__ uint32_t part[kFewThreads / 32];
   __shared__ float token_scale[kM];
   constexpr int kRows = kM >= 4 ? 2 : 1;  // channels of a warp at a time
   constexpr int kAhead = kM >= 4 ? 4 : 8;  // pieces of 16 bytes of each in flight per lane
@@ -520,48 +525,50 @@ __global__ void __launch_bounds__(kFewThreads)
   const int m = static_cast<int>(p.m);
   const int64_t step = static_cast<int64_t>(gridDim.x) * (kFewThreads / 32) * kRows;
   int64_t channel = (static_cast<int64_t>(blockIdx.x) * (kFewThreads / 32) + warp) * kRows;
+  const int whole = static_cast<int>(k / 16);  // pieces that end inside the row
   int4 w[kRows][kAhead];
   const auto load = [&](int64_t c0, int at) {
 #pragma unroll
-    for (int r = 0; r < kRows; ++r)
+    for (int r = 0; r < kRows; ++r) {
+      const int4* row = reinterpret_cast<const int4*>(B + min(c0 + r, p.n - 1) * ldb);
 #pragma unroll
       for (int i = 0; i < kAhead; ++i) {
         const int piece = at + lane + 32 * i;
-        w[r][i] = make_int4(0, 0, 0, 0);
-        if (piece < kp && c0 + r < p.n) w[r][i] = weights16(B + (c0 + r) * ldb, static_cast<int64_t>(piece) * 16, k);
+        w[r][i] = piece < whole ? __ldg(row + piece) : make_int4(0, 0, 0, 0);
       }
+    }
+    if (whole < kp) {  // the row's last bytes, one at a time
+#pragma unroll
+      for (int r = 0; r < kRows; ++r)
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i)
+          if (at + lane + 32 * i == whole)
+            w[r][i] = weights16(B + min(c0 + r, p.n - 1) * ldb, static_cast<int64_t>(whole) * 16, k);
+    }
   };
   load(channel, 0);
 
   if constexpr (kIn >= 0) {
     using T = typename Elem<kIn < 0 ? 0 : kIn>::T;
     const T* x = static_cast<const T*>(X);
-    uint32_t top[kM];
-#pragma unroll
-    for (int j = 0; j < kM; ++j) {
-      top[j] = 0;
-      if (j < m)
-        for (int64_t c = threadIdx.x * 8; c < k; c += kFewThreads * 8) {
-          float v[8];
-          load8<kIn < 0 ? 0 : kIn>(x + j * ldx, c, k, wide, v);
-#pragma unroll
-          for (int e = 0; e < 8; ++e) top[j] = max(top[j], __float_as_uint(v[e]) & 0x7fffffffu);
-        }
-      top[j] = __reduce_max_sync(0xffffffffu, top[j]);
-      if (lane == 0) part[warp][j] = top[j];
-    }
+    // the warps share the tokens out: 8 / kM of them to each
+    constexpr int kType1 = kIn < 0 ? 0 : kIn, kWarps = kFewThreads / 32 / kM;
+    const int j = warp / kWarps, first = warp % kWarps * 32 + lane;
+    const T* row = x + (j < m ? j : 0) * ldx;
+    Largest<kType1> top;
+#pragma unroll 4
+    for (int64_t c = first; c < 2 * kp; c += kWarps * 32) top.add(load8<kType1>(row, c * 8, k, wide));
+    const uint32_t mine = __reduce_max_sync(0xffffffffu, top.bits());
+    if (lane == 0) part[warp] = mine;
     __syncthreads();
-#pragma unroll
-    for (int j = 0; j < kM; ++j) {
-      if (j >= m) break;
-      const uint32_t a_bits = __reduce_max_sync(0xffffffffu, part[lane % (kFewThreads / 32)][j]);
-      const RowScale a = row_scale(a_bits);
-      if (threadIdx.x == 0) token_scale[j] = a.scale;
-      for (int64_t c = threadIdx.x * 8; c < static_cast<int64_t>(kp) * 16; c += kFewThreads * 8) {
+    const RowScale a = row_scale(__reduce_max_sync(0xffffffffu, part[j * kWarps + lane % kWarps]));
+    if (j < m) {
+      if (first == 0) token_scale[j] = a.scale;
+#pragma unroll 4
+      for (int64_t c = first; c < 2 * kp; c += kWarps * 32) {
         float v[8];
-        load8<kIn < 0 ? 0 : kIn>(x + j * ldx, c, k, wide, v);
-        const uint2 q = quantize8(v, a);
-        reinterpret_cast<uint2*>(tokens)[static_cast<int64_t>(j) * kp * 2 + c / 8] = q;
+        floats8<kType1>(load8<kType1>(row, c * 8, k, wide), v);
+        reinterpret_cast<uint2*>(tokens)[static_cast<int64_t>(j) * kp * 2 + c] = quantize8(v, a);
       }
     }
   } else {
