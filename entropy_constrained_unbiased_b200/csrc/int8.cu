@@ -42,27 +42,29 @@ __device__ __forceinline__ RowScale row_scale(uint32_t a_bits) {
 // quotient of a 31-bit by a 24-bit integer that is not a half differs from it by more
 // than an fp64 rounding). Adding 1.5 * 2^23 leaves the nearest integer in the low
 // bits, two's complement.
-__device__ __forceinline__ uint2 quantize8(const float (&v)[8], const RowScale& s) {
+__device__ __forceinline__ uint2 quantize8(float (&v)[8], const RowScale& s) {
   if (s.inv == 0.0f) return make_uint2(0, 0);
   constexpr float kInt = 12582912.0f;
+  constexpr float kClear = 0.5f - 0x1p-16f;
+  if (s.lift != 1.0f) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] *= s.lift;
+  }
   uint32_t b[8];
   float far = 0.0f;
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
-    const float t = __fmul_rn(v[e] * s.lift, s.inv), m = __fadd_rn(t, kInt);
+    const float t = __fmul_rn(v[e], s.inv), m = __fadd_rn(t, kInt);
     far = fmaxf(far, fabsf(t - __fadd_rn(m, -kInt)));
     b[e] = __float_as_uint(m);
   }
-  if (far > 0.5f - 0x1p-16f) {
-#pragma unroll 1
+  if (far > kClear) {
+    const double a = static_cast<double>(s.a) * static_cast<double>(s.lift);
+#pragma unroll
     for (int e = 0; e < 8; ++e) {
-      float x = v[0];
-#pragma unroll
-      for (int i = 1; i < 8; ++i) x = e == i ? v[i] : x;
-      const uint32_t q = static_cast<uint32_t>(
-          __double2int_rn(__ddiv_rn(static_cast<double>(x) * 127.0, static_cast<double>(s.a))));
-#pragma unroll
-      for (int i = 0; i < 8; ++i) b[i] = e == i ? q : b[i];
+      const float t = __fmul_rn(v[e], s.inv);
+      if (fabsf(t - rintf(t)) > kClear)
+        b[e] = static_cast<uint32_t>(__double2int_rn(__ddiv_rn(static_cast<double>(v[e]) * 127.0, a)));
     }
   }
   return make_uint2(__byte_perm(__byte_perm(b[0], b[1], 0x0040), __byte_perm(b[2], b[3], 0x0040), 0x5410),
@@ -70,7 +72,7 @@ __device__ __forceinline__ uint2 quantize8(const float (&v)[8], const RowScale& 
 }
 
 template <int kType, int kTPR, int kKeep, bool kLong>
-__global__ void __launch_bounds__(kTPR < 128 ? 128 : kTPR)
+__global__ void __launch_bounds__(kTPR < 128 ? 128 : kTPR, kTPR > 128 ? 3 : 1)
     k_int8_rows(const typename Elem<kType>::T* __restrict__ X, int64_t n, int64_t k, int64_t ldx, bool wide,
                 int8_t* __restrict__ Q, int64_t ldq, float* __restrict__ scale, int32_t* __restrict__ status) {
   constexpr int kThreads = kTPR < 128 ? 128 : kTPR;
@@ -340,6 +342,7 @@ cudaError_t int8_tile(const CUtensorMap& map_w, const CUtensorMap& map_x, const 
 // one is computed --
 
 constexpr int kPairStages = 6;
+constexpr int kPairThreads = 320;  // eight epilogue warps, the producer, the MMA issuer
 constexpr int kPairStage = 2 * 128 * kPieceK;  // each CTA: 128 rows of either operand
 constexpr int kPairSmem = kPairStages * kPairStage + 1024;
 
@@ -355,7 +358,7 @@ __device__ __forceinline__ TileAt tile_at(int t, int channel_tiles, int token_ti
 }
 
 template <int kType>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(192, 1)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     k_int8_pair(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_x, const Product p,
                 int channel_tiles, int token_tiles) {
   extern __shared__ unsigned char smem_raw[];
@@ -370,7 +373,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(192, 1)
   const int pair = static_cast<int>(blockIdx.x) >> 1, pairs = static_cast<int>(gridDim.x) >> 1;
   const int all = channel_tiles * token_tiles;
 
-  if (warp == 4) tmem_alloc<2>(smem_addr(&tmem_slot), 512);
+  if (warp == 8) tmem_alloc<2>(smem_addr(&tmem_slot), 512);
   if (threadIdx.x == 0) {
     prefetch_map(&map_w);
     prefetch_map(&map_x);
@@ -380,7 +383,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(192, 1)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(done + 8 * i, 1);
-      mbar_init(freed + 8 * i, 8);  // four warps of either CTA
+      mbar_init(freed + 8 * i, 16);  // eight warps of either CTA
     }
     fence_mbar_init();
   }
@@ -390,7 +393,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(192, 1)
   const uint32_t acc = __shfl_sync(0xffffffffu, tmem_slot, 0);
   bool ok = true;
 
-  if (warp == 4) {
+  if (warp == 8) {
     const bool elected = elect_one();
     const uint32_t full0 = map_shared(full, 0);
     Ring<kPairStages> at;
@@ -409,7 +412,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(192, 1)
       }
     }
     if (!ok && rank == 0) at.drain(full, kWaitLimit);
-  } else if (warp == 5) {
+  } else if (warp == 9) {
     if (rank == 0) {
       const bool elected = elect_one();
       Ring<kPairStages> at;
@@ -440,20 +443,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(192, 1)
     for (int t = pair; t < all; t += pairs, ++n) {
       const int buf = n & 1;
       const TileAt at = tile_at(t, channel_tiles, token_tiles);
-      const int64_t channel = static_cast<int64_t>(at.channel) * 256 + rank * 128 + warp * 32 + lane;
+      const int64_t channel = static_cast<int64_t>(at.channel) * 256 + rank * 128 + (warp & 3) * 32 + lane;
       const int64_t token0 = static_cast<int64_t>(at.token) * 256;
       const int tokens = static_cast<int>(min(static_cast<int64_t>(256), p.m - token0));
-      for (int j = threadIdx.x; j < tokens; j += 128) token_scale[buf][j] = p.sa[token0 + j];
+      for (int j = threadIdx.x; j < tokens; j += 256) token_scale[buf][j] = p.sa[token0 + j];
       const bool live = channel < p.n;
       const float s = live ? p.sb[channel] : 0.0f;
       const float bias = live && p.bias ? p.bias[channel] : 0.0f;
-      asm volatile("bar.sync 1, 128;" ::: "memory");
+      asm volatile("bar.sync 1, 256;" ::: "memory");
       ok = __all_sync(0xffffffffu, mbar_wait_bounded(done + 8 * buf, (n >> 1) & 1, kWaitLimit));
       if (!ok) break;
       tcgen05_after_sync();
-      for (int j0 = 0; j0 < tokens; j0 += 32) {
+      const int half = (warp >> 2) * 128, end = min(tokens, half + 128);  // this warp's tokens
+      for (int j0 = half; j0 < end; j0 += 32) {
         uint32_t v[32];
-        tmem_ld32(acc + (static_cast<uint32_t>(warp) << 21) + buf * 256 + j0, v);
+        tmem_ld32(acc + (static_cast<uint32_t>(warp & 3) << 21) + buf * 256 + j0, v);
         tcgen05_wait_ld();
         if (live) {
 #pragma unroll
@@ -471,7 +475,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(192, 1)
   __syncwarp();
   tcgen05_before_sync();
   cluster_sync_all();  // neither CTA leaves while the other's MMAs or copies use its memory
-  if (warp == 4) {
+  if (warp == 8) {
     tcgen05_after_sync();
     tmem_free<2>(acc, 512);
   }
@@ -484,7 +488,7 @@ cudaError_t int8_pair(const CUtensorMap& map_w, const CUtensorMap& map_x, const 
   const int64_t channel_tiles = (p.n + 255) / 256, token_tiles = (p.m + 255) / 256;
   if (channel_tiles * token_tiles > INT32_MAX / 32) return cudaErrorInvalidValue;
   const int pairs = static_cast<int>(std::min<int64_t>(sm_count() / 2, channel_tiles * token_tiles));
-  k_int8_pair<kType><<<2 * pairs, 192, kPairSmem, st>>>(map_w, map_x, p, static_cast<int>(channel_tiles),
+  k_int8_pair<kType><<<2 * pairs, kPairThreads, kPairSmem, st>>>(map_w, map_x, p, static_cast<int>(channel_tiles),
                                                        static_cast<int>(token_tiles));
   note_launch();
   return cudaGetLastError();
@@ -637,6 +641,10 @@ cudaError_t int8_few_tokens(const void* X, int64_t ldx, const int8_t* B, int64_t
 }
 
 bool few_tokens(int64_t m, int64_t k) { return m <= kFewTokens && m * ((k + 15) / 16 * 16) <= kFewBytes; }
+// Whether each CTA quantises the tokens itself: that repeats the work in every CTA, and
+// a second launch is cheaper for more entries (7 tokens of 4099 float32 entries: 26 us
+// in one kernel).
+bool few_entries(int64_t m, int64_t k) { return few_tokens(m, k) && m * k <= 8192; }
 
 // A map of 8-bit rows in boxes of 128 bytes by `rows`.
 bool map_rows8(CUtensorMap* map, const int8_t* p, int64_t n, int64_t k, int64_t ld, int rows) {
@@ -695,14 +703,14 @@ cudaError_t launch_int8_matmul(const int8_t* A, int64_t lda, const float* sa, co
 }
 
 size_t int8_linear_workspace(int64_t m, int64_t k) {
-  if (m == 0 || few_tokens(m, k)) return 0;
+  if (m == 0 || few_entries(m, k)) return 0;
   return static_cast<size_t>(m) * ((k + 31) / 32 * 32 + 8);  // integers, scales, status
 }
 
 cudaError_t launch_int8_linear(const void* X, int x_type, int64_t ldx, const int8_t* B, int64_t ldb, const float* sb,
                                const float* bias, int64_t m, int64_t n, int64_t k, void* Y, int64_t ldy, void* ws,
                                cudaStream_t st) {
-  if (few_tokens(m, k)) {
+  if (few_entries(m, k)) {
     const Product p = {nullptr, sb, bias, Y, m, n, ldy, 0};
     switch (x_type) {
       case kF32: return int8_few_tokens<kF32, kF32>(X, ldx, B, ldb, p, k, st);
