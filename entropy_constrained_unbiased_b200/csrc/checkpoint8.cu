@@ -71,19 +71,22 @@ __global__ void __launch_bounds__(256)
   uint32_t word[2] = {0, 0};
   if (b != kScaleNaN) {
     const uint32_t rnd[4] = {~u.x, ~u.y, ~u.z, ~u.w};  // 65535 - u in either half
-    const float up = __uint_as_float((254u - b) << 23) * 65536.0f;  // 2^16 / s, exact: b >= 17, or
-    const float inv = __uint_as_float((254u - b) << 23);            // in two steps for smaller s
-    const bool small = b < 17;
     float v[8];
     floats8<kType>(in, v);
+    uint32_t up_bits = (254u + 16u - b) << 23;  // 2^16 / s, a power of two
+    if (b < 17) {                               // beyond float32: in two exact steps
+      up_bits -= 64u << 23;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] *= 0x1p64f;
+    }
+    const float up = __uint_as_float(up_bits);
     const uint32_t* raw = reinterpret_cast<const uint32_t*>(&in);
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       uint32_t q[4];
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        const float x = fabsf(v[4 * h + e]);
-        const float z = small ? fmaf(x * inv, 65536.0f, 8388608.0f) : fmaf(x, up, 8388608.0f);
+        const float z = fmaf(fabsf(v[4 * h + e]), up, 8388608.0f);
         const uint32_t w = rnd[2 * h + (e >> 1)];
         q[e] = __float_as_uint(z) + ((e & 1) ? w >> 16 : w & 0xffffu);
       }
@@ -214,6 +217,7 @@ struct Gradient {
   int terms;          // bf16 terms of dY, the smallest first
   int split, per;     // parts of the token axis, pieces of one
   int chunk;          // pieces that one accumulator takes
+  bool early;         // launched behind the copy of dY's terms
 };
 
 // Two bytes of x as two's complement integers times s, in bf16. 0x4300 | b is the bf16
@@ -262,6 +266,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GradWarps<kExact>::k
   const int pair = static_cast<int>(blockIdx.x) >> 1, pairs = static_cast<int>(gridDim.x) >> 1;
   const int tiles = g.feature_tiles * g.output_tiles;
   const int all = tiles * g.split;
+  next_may_begin();
 
   if (warp == W::kLoad) tmem_alloc<2>(smem_addr(&tmem_slot), 512);
   if (threadIdx.x == 0) {
@@ -297,6 +302,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GradWarps<kExact>::k
     if (warp == W::kLoad) {
       const bool elected = elect_one();
       const uint32_t full0 = map_shared(full, 0);
+      after_previous();  // dY's terms; the integers do not wait for them
       Ring<kYStages> y;
       for (int w = pair; w < all && ok; w += pairs) {
         const int tile = w % tiles, part = w / tiles;
@@ -494,6 +500,7 @@ template <int kIn, int kTerms>
 __global__ void __launch_bounds__(256)
     k_terms(const typename Elem<kIn>::T* __restrict__ dY, int64_t ldy, bool wide, int64_t t, int64_t o,
             __nv_bfloat16* __restrict__ out, int64_t ld) {
+  next_may_begin();
   const int64_t r = static_cast<int64_t>(blockIdx.x) * blockDim.y + threadIdx.y;
   const int64_t c = static_cast<int64_t>(blockIdx.y) * blockDim.x + threadIdx.x;
   if (r >= t || c * 8 >= o) return;
@@ -520,6 +527,7 @@ template <int kOut>
 __global__ void __launch_bounds__(256)
     k_join(const float* __restrict__ part, int split, int64_t o, int64_t k, typename Elem<kOut>::T* __restrict__ dW,
            int64_t ldw) {
+  after_previous();
   const int64_t c = static_cast<int64_t>(blockIdx.y) * 256 + threadIdx.x, r = blockIdx.x;
   if (c >= k) return;
   float sum = 0.0f;
@@ -577,9 +585,9 @@ cudaError_t wgrad(const CUtensorMap& map_q, const CUtensorMap& map_s, const CUte
   if (e != cudaSuccess) return e;
   const int64_t all = static_cast<int64_t>(g.feature_tiles) * g.output_tiles * g.split;
   const int pairs = static_cast<int>(std::min<int64_t>(sm_count() / 2, all));
-  k_wgrad<kOut, kExact><<<2 * pairs, GradWarps<kExact>::kThreads, kGradSmem, st>>>(map_q, map_s, map_y, g);
   note_launch();
-  return cudaGetLastError();
+  return launch_kernel(k_wgrad<kOut, kExact>, dim3(2 * pairs), GradWarps<kExact>::kThreads, kGradSmem, st, 1, g.early,
+                       map_q, map_s, map_y, g);
 }
 
 template <int kOut>
@@ -597,10 +605,9 @@ cudaError_t wgrad_all(const CUtensorMap& map_q, const CUtensorMap& map_s, const 
   g.ld = g.k;
   const cudaError_t e = wgrad<kF32, kExact>(map_q, map_s, map_y, g, st);
   if (e != cudaSuccess) return e;
-  k_join<kOut><<<dim3(static_cast<unsigned>(g.o), static_cast<unsigned>((g.k + 255) / 256)), 256, 0, st>>>(
-      part, g.split, g.o, g.k, static_cast<typename Elem<kOut>::T*>(dW), ldw);
   note_launch();
-  return cudaGetLastError();
+  return launch_kernel(k_join<kOut>, dim3(static_cast<unsigned>(g.o), static_cast<unsigned>((g.k + 255) / 256)), 256, 0, st,
+                       1, true, part, g.split, g.o, g.k, static_cast<typename Elem<kOut>::T*>(dW), ldw);
 }
 
 }  // namespace
@@ -696,6 +703,7 @@ cudaError_t launch_checkpoint8_wgrad(const void* dY, int dy_type, int64_t ldy, c
   g.terms = p.terms;
   g.split = p.split;
   g.per = p.per;
+  g.early = p.copy;
   if (static_cast<int64_t>(g.feature_tiles) * g.output_tiles > INT32_MAX / 256) return cudaErrorInvalidValue;
   auto* part = reinterpret_cast<float*>(static_cast<unsigned char*>(ws) + p.terms_bytes);
   switch (dw_type) {

@@ -78,6 +78,7 @@ __global__ void __launch_bounds__(kTPR < 128 ? 128 : kTPR, kTPR > 128 ? 3 : 1)
   constexpr int kThreads = kTPR < 128 ? 128 : kTPR;
   constexpr int kRows = kThreads / kTPR;
   __shared__ uint32_t part[kThreads / 32];
+  next_may_begin();
   const int lane = threadIdx.x % kTPR;
   const int64_t r = static_cast<int64_t>(blockIdx.x) * kRows + threadIdx.x / kTPR;
   const bool live = r < n;
@@ -166,6 +167,7 @@ struct Product {
   void* Y;
   int64_t m, n, ldy;
   int pieces;  // ceil(k / 128)
+  bool early;  // launched behind the quantiser of the tokens
 };
 
 // One output: the exact integer sum, scaled.
@@ -228,14 +230,24 @@ __global__ void __launch_bounds__(192, 2)
 
   if (warp == 4) {
     const bool elected = elect_one();
+    // the first stages' weights do not wait for the quantiser
+    const int begun = min(count, Cfg::kStages);
+    if (elected)
+      for (int i = 0; i < begun; ++i) {
+        mbar_expect_tx(full + 8 * i, Cfg::kA + Cfg::kB);
+        tma_2d(tiles + i * (Cfg::kA + Cfg::kB), &map_w, (first + i) * kPieceK, channel0, full + 8 * i);
+      }
+    after_previous();
     Ring<Cfg::kStages> at;
     for (int i = 0; i < count; ++i, at.next()) {
       ok = __all_sync(0xffffffffu, at.wait_empty(empty, kWaitLimit));
       if (!ok) break;
       const uint32_t a = tiles + at.stage * (Cfg::kA + Cfg::kB), bar = full + 8 * at.stage;
       if (elected) {
-        mbar_expect_tx(bar, Cfg::kA + Cfg::kB);
-        tma_2d(a, &map_w, (first + i) * kPieceK, channel0, bar);
+        if (i >= begun) {
+          mbar_expect_tx(bar, Cfg::kA + Cfg::kB);
+          tma_2d(a, &map_w, (first + i) * kPieceK, channel0, bar);
+        }
         tma_2d(a + Cfg::kA, &map_x, (first + i) * kPieceK, token0, bar);
       }
     }
@@ -258,6 +270,7 @@ __global__ void __launch_bounds__(192, 2)
     }
     if (elected) mma_commit<1>(done);
   } else {
+    after_previous();
     ok = mbar_wait_bounded(done, 0, kWaitLimit);
     tcgen05_after_sync();
     const int64_t channel = channel0 + warp * 32 + lane;
@@ -322,19 +335,10 @@ cudaError_t int8_tile(const CUtensorMap& map_w, const CUtensorMap& map_x, const 
   const cudaError_t e = cudaFuncSetAttribute(k_int8_tile<kType, kTok>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::kSmem);
   if (e != cudaSuccess) return e;
   const int channel_tiles = static_cast<int>((p.n + 127) / 128);
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(channel_tiles * ((p.m + kTok - 1) / kTok) * split));
-  cfg.blockDim = dim3(192);
-  cfg.dynamicSmemBytes = Cfg::kSmem;
-  cfg.stream = st;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = static_cast<unsigned>(split);
-  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  const dim3 grid(static_cast<unsigned>(channel_tiles * ((p.m + kTok - 1) / kTok) * split));
   note_launch();
-  return cudaLaunchKernelEx(&cfg, k_int8_tile<kType, kTok>, map_w, map_x, p, channel_tiles, split);
+  return launch_kernel(k_int8_tile<kType, kTok>, grid, 192, Cfg::kSmem, st, static_cast<unsigned>(split), p.early, map_w,
+                       map_x, p, channel_tiles, split);
 }
 
 // -- many tokens: a pair of CTAs (cta_group::2) per 256 channels by 256 tokens,
@@ -396,6 +400,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
   if (warp == 8) {
     const bool elected = elect_one();
     const uint32_t full0 = map_shared(full, 0);
+    after_previous();
     Ring<kPairStages> at;
     for (int t = pair; t < all && ok; t += pairs) {
       const TileAt tile = tile_at(t, channel_tiles, token_tiles);
@@ -439,6 +444,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
       }
     }
   } else {
+    after_previous();
     int n = 0;
     for (int t = pair; t < all; t += pairs, ++n) {
       const int buf = n & 1;
@@ -488,10 +494,9 @@ cudaError_t int8_pair(const CUtensorMap& map_w, const CUtensorMap& map_x, const 
   const int64_t channel_tiles = (p.n + 255) / 256, token_tiles = (p.m + 255) / 256;
   if (channel_tiles * token_tiles > INT32_MAX / 32) return cudaErrorInvalidValue;
   const int pairs = static_cast<int>(std::min<int64_t>(sm_count() / 2, channel_tiles * token_tiles));
-  k_int8_pair<kType><<<2 * pairs, kPairThreads, kPairSmem, st>>>(map_w, map_x, p, static_cast<int>(channel_tiles),
-                                                       static_cast<int>(token_tiles));
   note_launch();
-  return cudaGetLastError();
+  return launch_kernel(k_int8_pair<kType>, dim3(2 * pairs), kPairThreads, kPairSmem, st, 1, p.early, map_w, map_x, p,
+                       static_cast<int>(channel_tiles), static_cast<int>(token_tiles));
 }
 
 // -- up to 8 tokens: the weights' bytes are the cost, and one launch. Each CTA holds
@@ -576,6 +581,7 @@ __global__ void __launch_bounds__(kFewThreads)
       }
     }
   } else {
+    after_previous();
     const int8_t* x = static_cast<const int8_t*>(X);
     for (int j = 0; j < m; ++j)
       for (int c = threadIdx.x; c < kp; c += kFewThreads)
@@ -630,9 +636,9 @@ cudaError_t int8_few_tokens(const void* X, int64_t ldx, const int8_t* B, int64_t
       if (e != cudaSuccess) return e;
     }
     const int64_t per = kFewThreads / 32 * rows, most = static_cast<int64_t>(sm_count()) * 4;
-    kernel<<<static_cast<unsigned>(std::min((p.n + per - 1) / per, most)), kFewThreads, smem, st>>>(X, ldx, wide, B, ldb, p, k);
     note_launch();
-    return cudaGetLastError();
+    return launch_kernel(kernel, dim3(static_cast<unsigned>(std::min((p.n + per - 1) / per, most))), kFewThreads, smem, st,
+                         1, p.early, X, ldx, wide, B, ldb, p, k);
   };
   if (p.m == 1) return run(k_int8_few<kIn, kType, 1>, 1);
   if (p.m == 2) return run(k_int8_few<kIn, kType, 2>, 1);
@@ -691,15 +697,23 @@ cudaError_t launch_int8_quantize(const void* X, int type, int64_t n, int64_t k, 
   }
 }
 
-cudaError_t launch_int8_matmul(const int8_t* A, int64_t lda, const float* sa, const int8_t* B, int64_t ldb,
-                               const float* sb, const float* bias, int64_t m, int64_t n, int64_t k, void* Y, int type,
-                               int64_t ldy, cudaStream_t st) {
-  const Product p = {sa, sb, bias, Y, m, n, ldy, static_cast<int>((k + kPieceK - 1) / kPieceK)};
+namespace {
+cudaError_t int8_matmul(const int8_t* A, int64_t lda, const float* sa, const int8_t* B, int64_t ldb, const float* sb,
+                        const float* bias, int64_t m, int64_t n, int64_t k, void* Y, int type, int64_t ldy, bool early,
+                        cudaStream_t st) {
+  const Product p = {sa, sb, bias, Y, m, n, ldy, static_cast<int>((k + kPieceK - 1) / kPieceK), early};
   switch (type) {
     case kF32: return int8_product<kF32>(A, lda, B, ldb, p, k, st);
     case kBF16: return int8_product<kBF16>(A, lda, B, ldb, p, k, st);
     default: return int8_product<kF16>(A, lda, B, ldb, p, k, st);
   }
+}
+}  // namespace
+
+cudaError_t launch_int8_matmul(const int8_t* A, int64_t lda, const float* sa, const int8_t* B, int64_t ldb,
+                               const float* sb, const float* bias, int64_t m, int64_t n, int64_t k, void* Y, int type,
+                               int64_t ldy, cudaStream_t st) {
+  return int8_matmul(A, lda, sa, B, ldb, sb, bias, m, n, k, Y, type, ldy, false, st);
 }
 
 size_t int8_linear_workspace(int64_t m, int64_t k) {
@@ -711,7 +725,7 @@ cudaError_t launch_int8_linear(const void* X, int x_type, int64_t ldx, const int
                                const float* bias, int64_t m, int64_t n, int64_t k, void* Y, int64_t ldy, void* ws,
                                cudaStream_t st) {
   if (few_entries(m, k)) {
-    const Product p = {nullptr, sb, bias, Y, m, n, ldy, 0};
+    const Product p = {nullptr, sb, bias, Y, m, n, ldy, 0, false};
     switch (x_type) {
       case kF32: return int8_few_tokens<kF32, kF32>(X, ldx, B, ldb, p, k, st);
       case kBF16: return int8_few_tokens<kBF16, kBF16>(X, ldx, B, ldb, p, k, st);
@@ -724,7 +738,7 @@ cudaError_t launch_int8_linear(const void* X, int x_type, int64_t ldx, const int
   const cudaError_t e =
       launch_int8_quantize(X, x_type, m, k, ldx, q, ldq, scale, reinterpret_cast<int32_t*>(scale + m), st);
   if (e != cudaSuccess) return e;
-  return launch_int8_matmul(q, ldq, scale, B, ldb, sb, bias, m, n, k, Y, x_type, ldy, st);
+  return int8_matmul(q, ldq, scale, B, ldb, sb, bias, m, n, k, Y, x_type, ldy, true, st);
 }
 
 cudaError_t int8_stalled(bool* stalled) {
