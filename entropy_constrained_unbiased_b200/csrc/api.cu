@@ -78,8 +78,8 @@ size_t approx_ws(void* ws, int n, int p, const ApproxPlan& plan, SolveWs* w) {
 }
 
 // 8-bit operators: element type, sizes and the layout of an 8-bit matrix.
-constexpr int64_t kMaxRows8 = INT32_MAX;
-constexpr int64_t kMaxCols8 = int64_t(1) << 27;
+constexpr int64_t kMaxRows8 = INT32_MAX - 1023;  // coordinates of the last tile stay below 2^31
+constexpr int64_t kMaxCols8 = int64_t(1) << 26;
 constexpr int64_t kMaxK8 = 131072;  // 127^2 * 131072 < 2^31
 
 bool valid_type(int type) { return type == ECASQ_F32 || type == ECASQ_BF16 || type == ECASQ_F16; }

@@ -528,20 +528,27 @@ __global__ void __launch_bounds__(256)
     k_join(const float* __restrict__ part, int split, int64_t o, int64_t k, typename Elem<kOut>::T* __restrict__ dW,
            int64_t ldw) {
   after_previous();
-  const int64_t c = static_cast<int64_t>(blockIdx.y) * 256 + threadIdx.x, r = blockIdx.x;
+  const int64_t c = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
   if (c >= k) return;
-  float sum = 0.0f;
-  const float* from = part + r * k + c;
+  for (int64_t r = blockIdx.y; r < o; r += gridDim.y) {
+    float sum = 0.0f;
+    const float* from = part + r * k + c;
 #pragma unroll 8
-  for (int i = 0; i < split; ++i) sum += __ldg(from + i * (o * k));
-  dW[r * ldw + c] = Elem<kOut>::put(sum);
+    for (int i = 0; i < split; ++i) sum += __ldg(from + i * (o * k));
+    dW[r * ldw + c] = Elem<kOut>::put(sum);
+  }
+}
+
+// The grid of kernels with 256 columns per CTA that walk the rows.
+dim3 column_grid(int64_t o, int64_t k) {
+  return dim3(static_cast<unsigned>((k + 255) / 256), static_cast<unsigned>(std::min<int64_t>(o, 65535)));
 }
 
 template <int kOut>
 __global__ void __launch_bounds__(256)
-    k_zero(int64_t k, typename Elem<kOut>::T* __restrict__ dW, int64_t ldw) {
-  const int64_t c = static_cast<int64_t>(blockIdx.y) * 256 + threadIdx.x;
-  if (c < k) dW[static_cast<int64_t>(blockIdx.x) * ldw + c] = Elem<kOut>::put(0.0f);
+    k_zero(int64_t o, int64_t k, typename Elem<kOut>::T* __restrict__ dW, int64_t ldw) {
+  const int64_t c = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+  for (int64_t r = blockIdx.y; r < o && c < k; r += gridDim.y) dW[r * ldw + c] = Elem<kOut>::put(0.0f);
 }
 
 // How a gradient is cut: bf16 terms and whether dY is copied into them, parts of the
@@ -606,8 +613,7 @@ cudaError_t wgrad_all(const CUtensorMap& map_q, const CUtensorMap& map_s, const 
   const cudaError_t e = wgrad<kF32, kExact>(map_q, map_s, map_y, g, st);
   if (e != cudaSuccess) return e;
   note_launch();
-  return launch_kernel(k_join<kOut>, dim3(static_cast<unsigned>(g.o), static_cast<unsigned>((g.k + 255) / 256)), 256, 0, st,
-                       1, true, part, g.split, g.o, g.k, static_cast<typename Elem<kOut>::T*>(dW), ldw);
+  return launch_kernel(k_join<kOut>, column_grid(g.o, g.k), 256, 0, st, 1, true, part, g.split, g.o, g.k, static_cast<typename Elem<kOut>::T*>(dW), ldw);
 }
 
 }  // namespace
@@ -660,13 +666,13 @@ cudaError_t launch_checkpoint8_wgrad(const void* dY, int dy_type, int64_t ldy, c
                                      const uint8_t* scale, int64_t lds, int64_t t, int64_t o, int64_t k, void* dW,
                                      int dw_type, int64_t ldw, void* ws, cudaStream_t st) {
   if (t == 0) {
-    const dim3 grid(static_cast<unsigned>(o), static_cast<unsigned>((k + 255) / 256));
+    const dim3 grid = column_grid(o, k);
     if (dw_type == kF32)
-      k_zero<kF32><<<grid, 256, 0, st>>>(k, static_cast<float*>(dW), ldw);
+      k_zero<kF32><<<grid, 256, 0, st>>>(o, k, static_cast<float*>(dW), ldw);
     else if (dw_type == kBF16)
-      k_zero<kBF16><<<grid, 256, 0, st>>>(k, static_cast<__nv_bfloat16*>(dW), ldw);
+      k_zero<kBF16><<<grid, 256, 0, st>>>(o, k, static_cast<__nv_bfloat16*>(dW), ldw);
     else
-      k_zero<kF16><<<grid, 256, 0, st>>>(k, static_cast<__half*>(dW), ldw);
+      k_zero<kF16><<<grid, 256, 0, st>>>(o, k, static_cast<__half*>(dW), ldw);
     note_launch();
     return cudaGetLastError();
   }

@@ -525,10 +525,11 @@ def _vector(t, name, n, index):
     return t.data_ptr()
 
 
-def _rows8(n, k, to, dtype, device):
-    """Uninitialised 8-bit values in rows of a whole number of `to` bytes: all of them, and the [n, k] part."""
+def _rows8(like, n, k, to, dtype):
+    """Uninitialised 8-bit values on like's device in rows of a whole number of `to` bytes: all of them, and the
+    [n, k] part."""
     kp = (k + to - 1) // to * to
-    t = torch.empty((n, kp), dtype=dtype, device=device)
+    t = like.new_empty((n, kp), dtype=dtype)
     return t, (t if kp == k else t[:, :k])
 
 
@@ -548,10 +549,9 @@ def int8_quantize(X: torch.Tensor):
         with torch.cuda.device(index):
             return int8_quantize(X)
     n, k, ld = _matrix(X, "X", _TYPES)
-    dev = X.device
-    rows, q = _rows8(n, k, 32, torch.int8, dev)
-    scale = torch.empty(n, dtype=torch.float32, device=dev)
-    st = torch.empty(n, dtype=torch.int32, device=dev)
+    rows, q = _rows8(X, n, k, 32, torch.int8)
+    scale = X.new_empty(n, dtype=torch.float32)
+    st = X.new_empty(n, dtype=torch.int32)
     rc = _lib.ecasq_int8_quantize(X.data_ptr(), _TYPES[X.dtype], n, k, ld, rows.data_ptr(), rows.shape[1],
                                   scale.data_ptr(), st.data_ptr(), _stream_of(index))
     if rc:
@@ -583,7 +583,7 @@ def int8_matmul(A: torch.Tensor, sa: torch.Tensor, B: torch.Tensor, sb: torch.Te
     n, ldb, sbp, biasp = _weights(B, sb, bias, k, index)
     if out_dtype not in _TYPES:
         raise EcasqError(f"out_dtype must be float32, bfloat16 or float16, not {out_dtype}")
-    Y = torch.empty((m, n), dtype=out_dtype, device=A.device)
+    Y = A.new_empty((m, n), dtype=out_dtype)
     rc = _lib.ecasq_int8_matmul(A.data_ptr(), lda, _vector(sa, "sa", m, index), B.data_ptr(), ldb, sbp, biasp, m, n, k,
                                 Y.data_ptr(), _TYPES[out_dtype], n, _stream_of(index))
     if rc:
@@ -607,7 +607,7 @@ def int8_linear(X: torch.Tensor, B: torch.Tensor, sb: torch.Tensor, bias=None):
     n, ldb, sbp, biasp = _weights(B, sb, bias, k, index)
     Y = X.new_empty((m, n))
     need = _linear_workspace(m, k)
-    ws = torch.empty(need, dtype=torch.uint8, device=X.device) if need else None
+    ws = X.new_empty(need, dtype=torch.uint8) if need else None
     rc = _lib.ecasq_int8_linear(X.data_ptr(), _TYPES[X.dtype], ld, B.data_ptr(), ldb, sbp, biasp, m, n, k, Y.data_ptr(),
                                 n, ws.data_ptr() if need else None, need, _stream_of(index))
     if rc:
@@ -630,9 +630,10 @@ def checkpoint8(X: torch.Tensor, seed):
         if seed.dtype != torch.int64 or seed.numel() != 1 or seed.get_device() != index:
             raise EcasqError(f"a seed tensor must hold one int64 on cuda:{index}")
         seed, word = 0, seed.data_ptr()
-    dev = X.device
-    q_rows, q = _rows8(t, k, 32, torch.int8, dev)
-    s_rows, s = _rows8(t, (k + 31) // 32, 16, torch.uint8, dev)
+    elif not isinstance(seed, int):
+        raise EcasqError(f"seed must be an integer or a CUDA int64 tensor of one entry, not {type(seed).__name__}")
+    q_rows, q = _rows8(X, t, k, 32, torch.int8)
+    s_rows, s = _rows8(X, t, (k + 31) // 32, 16, torch.uint8)
     rc = _lib.ecasq_checkpoint8(X.data_ptr(), _TYPES[X.dtype], t, k, ld, seed & 0xFFFFFFFFFFFFFFFF, word,
                                 q_rows.data_ptr(), q_rows.shape[1], s_rows.data_ptr(), s_rows.shape[1],
                                 _stream_of(index))
@@ -658,7 +659,7 @@ def checkpoint8_restore(q: torch.Tensor, scale: torch.Tensor, dtype=torch.float3
     t, k, ldq, lds = _checkpoint(q, scale)
     if dtype not in _TYPES:
         raise EcasqError(f"dtype must be float32, bfloat16 or float16, not {dtype}")
-    X = torch.empty((t, k), dtype=dtype, device=q.device)
+    X = q.new_empty((t, k), dtype=dtype)
     rc = _lib.ecasq_checkpoint8_restore(q.data_ptr(), ldq, scale.data_ptr(), lds, t, k, X.data_ptr(), _TYPES[dtype], k,
                                         _stream_of(index))
     if rc:
@@ -687,10 +688,10 @@ def checkpoint8_wgrad(dY: torch.Tensor, q: torch.Tensor, scale: torch.Tensor, ou
         out_dtype = dY.dtype
     elif out_dtype not in _TYPES:
         raise EcasqError(f"out_dtype must be float32, bfloat16 or float16, not {out_dtype}")
-    dW = torch.empty((o, k), dtype=out_dtype, device=dY.device)
+    dW = dY.new_empty((o, k), dtype=out_dtype)
     at = dY.data_ptr()
     need = _wgrad_workspace(index, at % 16, ty, ldy, t, o, k)
-    ws = torch.empty(need, dtype=torch.uint8, device=dY.device) if need else None
+    ws = dY.new_empty(need, dtype=torch.uint8) if need else None
     rc = _lib.ecasq_checkpoint8_wgrad(at, ty, ldy, q.data_ptr(), ldq, scale.data_ptr(), lds, t, o, k, dW.data_ptr(),
                                       _TYPES[out_dtype], k, ws.data_ptr() if need else None, need, _stream_of(index))
     if rc:

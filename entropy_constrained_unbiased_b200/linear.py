@@ -18,6 +18,14 @@ import torch.nn.functional as F
 from . import ecasq as E
 
 
+def _rows(x):
+    """x [..., k] as a matrix with adjacent columns and distinct rows: a view, or a copy of a transposed or expanded x."""
+    rows = x if x.dim() == 2 else x.reshape(-1, x.shape[-1])
+    n, k = rows.shape
+    ld, one = rows.stride()
+    return rows.contiguous() if (k > 1 and one != 1) or (n > 1 and ld < k) else rows
+
+
 def int8_linear(x: torch.Tensor, weight: torch.Tensor, weight_scale: torch.Tensor, bias=None) -> torch.Tensor:
     """x [..., k] (float32, bfloat16 or float16) times 8-bit weights: quantises each
     token and multiplies, Y [..., n] in x's type. weight int8 [n, k] and
@@ -26,19 +34,18 @@ def int8_linear(x: torch.Tensor, weight: torch.Tensor, weight_scale: torch.Tenso
     that asks for one."""
     if x.requires_grad and torch.is_grad_enabled():
         raise E.EcasqError("int8_linear has no gradient; use checkpoint_linear for training, or torch.no_grad()")
-    if x.dim() == 2:
-        return E.int8_linear(x, weight, weight_scale, bias)
-    y = E.int8_linear(x.reshape(-1, x.shape[-1]), weight, weight_scale, bias)
-    return y.reshape(*x.shape[:-1], y.shape[1])
+    if x.dim() == 0:
+        raise E.EcasqError("x must have at least one dimension")
+    y = E.int8_linear(_rows(x), weight, weight_scale, bias)
+    return y if x.dim() == 2 else y.reshape(*x.shape[:-1], y.shape[1])
 
 
 class _CheckpointLinear(torch.autograd.Function):
     @staticmethod
     @torch.amp.custom_fwd(device_type="cuda")
     def forward(ctx, x, weight, bias, seed):
-        ctx.rows = x.shape[:-1]
         if ctx.needs_input_grad[1]:
-            q, scale = E.checkpoint8(x.reshape(-1, x.shape[-1]), seed)
+            q, scale = E.checkpoint8(_rows(x), seed)
         else:
             q = scale = None
         ctx.save_for_backward(q, scale, weight if ctx.needs_input_grad[0] else None)
@@ -54,10 +61,8 @@ class _CheckpointLinear(torch.autograd.Function):
         dx = dw = db = None
         if ctx.needs_input_grad[0]:
             dx = torch.matmul(dy, weight).to(x_type)
-        rows = dy.reshape(-1, dy.shape[-1])
+        rows = _rows(dy)
         if ctx.needs_input_grad[1]:
-            if rows.stride(1) != 1 or (rows.shape[0] > 1 and rows.stride(0) < rows.shape[1]):
-                rows = rows.contiguous()  # an expanded gradient, such as that of a sum
             dw = E.checkpoint8_wgrad(rows, q, scale, w_type)
         if ctx.needs_input_grad[2]:
             db = rows.sum(0, dtype=torch.float32).to(b_type)
@@ -68,7 +73,10 @@ def checkpoint_linear(x: torch.Tensor, weight: torch.Tensor, bias=None, *, seed)
     """x [..., k] W^T + bias, keeping x for the backward pass in 8 bits (unbiased,
     keyed by `seed`: another value for each layer and step, so that roundings are
     independent; an integer, or a CUDA int64 tensor of one entry for graphs).
-    weight [n, k] and bias [n] in x's type, or in any under autocast."""
+    weight [n, k] and bias [n] in x's type, or in any under autocast.
+
+    A backward pass may be captured into a graph, as with F.linear: warm up on the
+    capturing stream, and keep no eager autograd graph of the same leaves alive."""
     if x.device.type != "cuda" or weight.device != x.device:
         raise E.EcasqError("checkpoint_linear needs x and weight on one CUDA device; there is no CPU path")
     if weight.dim() != 2 or x.dim() < 1 or x.shape[-1] != weight.shape[1]:

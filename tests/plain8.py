@@ -13,10 +13,10 @@ def int8_rows(x):
     return q.astype(np.int8), scale.astype(np.float32), bad
 
 
-def philox(seed, rows, n):
-    """Words of the Philox4x32-10 blocks 0 .. n-1 of each row, third counter word 2: [rows, n, 4] uint64."""
+def philox(seed, rows, n, row0=0):
+    """Words of the Philox4x32-10 blocks 0 .. n-1 of rows row0 and on, third counter word 2: [rows, n, 4] uint64."""
     u, low = np.uint64, np.uint64(0xFFFFFFFF)
-    c = [np.broadcast_to(np.arange(n, dtype=u), (rows, n)), np.broadcast_to(np.arange(rows, dtype=u)[:, None], (rows, n)),
+    c = [np.broadcast_to(np.arange(n, dtype=u), (rows, n)), np.broadcast_to(np.arange(row0, row0 + rows, dtype=u)[:, None], (rows, n)),
          np.full((rows, n), 2, u), np.zeros((rows, n), u)]
     k0, k1 = seed & 0xFFFFFFFF, seed >> 32 & 0xFFFFFFFF
     for _ in range(10):
@@ -26,8 +26,8 @@ def philox(seed, rows, n):
     return np.stack(c, -1)
 
 
-def checkpoint(x, seed):
-    """q int8 [t, k] and scale bytes [t, blocks] of x [t, k] float64."""
+def checkpoint(x, seed, row0=0):
+    """q int8 [t, k] and scale bytes [t, blocks] of x [t, k] float64, rows row0 and on of a matrix."""
     t, k = x.shape
     blocks = (k + 31) // 32
     full = np.zeros((t, blocks * 32))
@@ -41,7 +41,7 @@ def checkpoint(x, seed):
     bad = ~(top <= 127 * 2.0**121)
     b = np.where(bad, 255, e + 127).astype(np.uint8)
     z = np.where(bad[:, :, None], 0, size) / np.exp2(e)[:, :, None]
-    w = philox(seed, t, blocks * 4)
+    w = philox(seed, t, blocks * 4, row0)
     u = np.stack([w & np.uint64(0xFFFF), w >> np.uint64(16)], -1).reshape(z.shape).astype(np.float64)
     low = np.floor(z)
     q = np.where(full < 0, -1, 1) * (low + (u < np.rint((z - low) * 65536)))

@@ -366,3 +366,65 @@ def test_training_and_serving_together(E):
         y = torch.relu(x @ w1.T) @ w2.T
         y8 = int8_linear(torch.relu(int8_linear(x, q1, s1)), q2, s2)
     assert (y8 - y).norm() <= 0.05 * y.norm()
+
+
+def test_linear_of_transposed_and_expanded_inputs(E):
+    from entropy_constrained_unbiased_b200.linear import checkpoint_linear, int8_linear
+    base = _x(1, 64, 20, torch.float32)
+    w = _x(2, 10, 64, torch.float32).requires_grad_()
+    wq, ws, _ = E.int8_quantize(w.detach())
+    for x in (base.T, base[:, :1].T.expand(20, 64), base.T.reshape(4, 5, 64).transpose(0, 1)):
+        y = checkpoint_linear(x, w, seed=1)
+        c = _x(3, y.numel(), 1, torch.float32).reshape(y.shape)
+        (dw,) = torch.autograd.grad(y, w, c)
+        q, b = E.checkpoint8(x.reshape(-1, 64).contiguous(), 1)
+        assert torch.equal(dw, E.checkpoint8_wgrad(c.reshape(-1, 10), q, b))
+        assert torch.equal(int8_linear(x, wq, ws), int8_linear(x.contiguous(), wq, ws))
+
+
+def test_training_step_in_a_graph(E):
+    """Forward and backward captured once and replayed with new inputs and a new seed word equal the eager step."""
+    from entropy_constrained_unbiased_b200.linear import checkpoint_linear
+    x, w = _x(1, 96, 64, torch.bfloat16), _x(2, 40, 64, torch.bfloat16).requires_grad_()
+    c, word = _x(3, 96, 40, torch.bfloat16), torch.tensor([9], device="cuda")
+    step = lambda seed: torch.autograd.grad(checkpoint_linear(x, w, seed=seed), w, c)[0]
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step(word)
+    torch.cuda.current_stream().wait_stream(side)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        dw = step(word)
+    for seed in (9, 10):
+        word.fill_(seed)
+        x.copy_(_x(seed, 96, 64, torch.bfloat16))
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(dw, step(seed))
+
+
+def test_offsets_past_32_bits(E):
+    """More than 2^31 entries: the last rows of every operator equal those of the rows alone (the checkpoint's
+    random bits go by the row's number, so its rows are compared with the definition)."""
+    t, k = 70001, 32768
+    X = torch.empty((t, k), dtype=torch.bfloat16, device="cuda")
+    X.normal_(generator=torch.Generator("cuda").manual_seed(1))
+    q, b = E.checkpoint8(X, 5)
+    x = E.checkpoint8_restore(q, b, torch.bfloat16)
+    want = plain8.checkpoint(_f64(X[-2:]), 5, t - 2)
+    np.testing.assert_array_equal(q[-2:].cpu().numpy(), want[0])
+    np.testing.assert_array_equal(b[-2:].cpu().numpy(), want[1])
+    np.testing.assert_array_equal(_f64(x[-2:]), plain8.values(*want))
+    dY = torch.zeros((t, 8), dtype=torch.bfloat16, device="cuda")
+    dY[-2:] = _x(2, 2, 8, torch.bfloat16)
+    dW = E.checkpoint8_wgrad(dY, q, b, torch.float32)
+    ref = _f64(dY[-2:]).T @ plain8.values(*want)
+    assert np.all(np.abs(_f64(dW) - ref) <= 2.0**-22 * (np.abs(_f64(dY[-2:])).T @ np.abs(plain8.values(*want))) + 1e-30)
+    del x, q, b, dY, dW
+    a, s, _ = E.int8_quantize(X)
+    last, ls, _ = E.int8_quantize(X[-3:].clone())
+    assert torch.equal(a[-3:], last) and torch.equal(s[-3:], ls)
+    B, sb, _ = E.int8_quantize(_x(3, 24, k, torch.float32))
+    assert torch.equal(E.int8_matmul(a, s, B, sb)[-3:], E.int8_matmul(last, ls, B, sb))
+    assert torch.equal(E.int8_matmul(B, sb, a, s)[:, -3:], E.int8_matmul(B, sb, last, ls))

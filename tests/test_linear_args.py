@@ -113,7 +113,7 @@ def test_binding_refusals():
         lambda: E.int8_matmul(q, s, q, s.double()), lambda: E.int8_matmul(q, s, q, s, s.bfloat16()),
         lambda: E.int8_matmul(q[:, 8:], s, q[:, 8:], s), lambda: E.int8_matmul(q, s, q[:0], s[:0]),
         lambda: E.int8_matmul(q, s.cpu(), q, s), lambda: E.int8_matmul(q, s, q, s, out_dtype=torch.float64),
-        lambda: E.checkpoint8(x, torch.tensor([1])), lambda: E.checkpoint8(x, torch.zeros(2, dtype=torch.int64, device="cuda")),
+        lambda: E.checkpoint8(x, torch.tensor([1])), lambda: E.checkpoint8(x, 1.5), lambda: E.checkpoint8(x, None), lambda: E.checkpoint8(x, torch.zeros(2, dtype=torch.int64, device="cuda")),
         lambda: E.checkpoint8_restore(c, b[:, :1]), lambda: E.checkpoint8_restore(c, b, torch.int8),
         lambda: E.checkpoint8_restore(odd, b), lambda: E.checkpoint8_wgrad(x[:3], c, b),
         lambda: E.checkpoint8_wgrad(x.double(), c, b), lambda: E.checkpoint8_wgrad(x, c, b, torch.int32),
