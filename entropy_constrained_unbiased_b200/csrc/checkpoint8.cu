@@ -533,7 +533,7 @@ __global__ void __launch_bounds__(256)
   for (int64_t r = blockIdx.y; r < o; r += gridDim.y) {
     float sum = 0.0f;
     const float* from = part + r * k + c;
-#pragma unroll 8
+#pragma unroll 16
     for (int i = 0; i < split; ++i) sum += __ldg(from + i * (o * k));
     dW[r * ldw + c] = Elem<kOut>::put(sum);
   }

@@ -508,17 +508,6 @@ constexpr int kFewTokens = 8;
 constexpr int64_t kFewBytes = 64 << 10;  // shared memory of the tokens
 constexpr int kFewThreads = 256;
 
-// 16 bytes of a row of weights, zeros beyond k.
-__device__ __forceinline__ int4 weights16(const int8_t* __restrict__ row, int64_t at, int64_t k) {
-  if (at + 16 <= k) return __ldg(reinterpret_cast<const int4*>(row + at));
-  int4 v = make_int4(0, 0, 0, 0);
-  int* w = reinterpret_cast<int*>(&v);
-#pragma unroll
-  for (int e = 0; e < 16; ++e)
-    if (at + e < k) w[e >> 2] |= (row[at + e] & 0xff) << (8 * (e & 3));
-  return v;
-}
-
 // kIn: the tokens' type, or -1 for rows that are quantised already (A, sa).
 template <int kIn, int kType, int kM>
 __global__ void __launch_bounds__(kFewThreads)
@@ -527,33 +516,24 @@ __global__ void __launch_bounds__(kFewThreads)
   extern __shared__ int4 tokens[];  // [m][kp / 16]
   __shared__ uint32_t part[kFewThreads / 32];
   __shared__ float token_scale[kM];
-  constexpr int kRows = kM >= 4 ? 2 : 1;  // channels of a warp at a time
-  constexpr int kAhead = kM >= 4 ? 4 : 8;  // pieces of 16 bytes of each in flight per lane
+  constexpr int kAhead = 8;  // pieces of 16 bytes in flight per lane
   const int warp = warp_id(), lane = lane_id();
   const int kp = static_cast<int>((k + 15) / 16);
   const int m = static_cast<int>(p.m);
-  const int64_t step = static_cast<int64_t>(gridDim.x) * (kFewThreads / 32) * kRows;
-  int64_t channel = (static_cast<int64_t>(blockIdx.x) * (kFewThreads / 32) + warp) * kRows;
+  const int64_t step = static_cast<int64_t>(gridDim.x) * (kFewThreads / 32);
+  int64_t channel = static_cast<int64_t>(blockIdx.x) * (kFewThreads / 32) + warp;
   const int whole = static_cast<int>(k / 16);  // pieces that end inside the row
-  int4 w[kRows][kAhead];
-  const auto load = [&](int64_t c0, int at) {
+  const int tail = static_cast<int>(k) - whole * 16;  // bytes of the last, short piece: one per lane
+  int4 w[kAhead];
+  int last = 0;
+  const auto load = [&](int64_t c, int at) {
+    const int8_t* row = B + min(c, p.n - 1) * ldb;
 #pragma unroll
-    for (int r = 0; r < kRows; ++r) {
-      const int4* row = reinterpret_cast<const int4*>(B + min(c0 + r, p.n - 1) * ldb);
-#pragma unroll
-      for (int i = 0; i < kAhead; ++i) {
-        const int piece = at + lane + 32 * i;
-        w[r][i] = piece < whole ? __ldg(row + piece) : make_int4(0, 0, 0, 0);
-      }
+    for (int i = 0; i < kAhead; ++i) {
+      const int piece = at + lane + 32 * i;
+      w[i] = piece < whole ? __ldg(reinterpret_cast<const int4*>(row) + piece) : make_int4(0, 0, 0, 0);
     }
-    if (whole < kp) {  // the row's last bytes, one at a time
-#pragma unroll
-      for (int r = 0; r < kRows; ++r)
-#pragma unroll
-        for (int i = 0; i < kAhead; ++i)
-          if (at + lane + 32 * i == whole)
-            w[r][i] = weights16(B + min(c0 + r, p.n - 1) * ldb, static_cast<int64_t>(whole) * 16, k);
-    }
+    if (at == 0 && lane < tail) last = __ldg(row + whole * 16 + lane);
   };
   load(channel, 0);
 
@@ -583,45 +563,50 @@ __global__ void __launch_bounds__(kFewThreads)
   } else {
     after_previous();
     const int8_t* x = static_cast<const int8_t*>(X);
-    for (int j = 0; j < m; ++j)
-      for (int c = threadIdx.x; c < kp; c += kFewThreads)
-        tokens[j * kp + c] = weights16(x + j * ldx, static_cast<int64_t>(c) * 16, k);
+#pragma unroll 8
+    for (int i = threadIdx.x; i < m * kp; i += kFewThreads) {
+      const int j = i / kp, c = i - j * kp;
+      if (c < whole) tokens[i] = __ldg(reinterpret_cast<const int4*>(x + j * ldx) + c);
+    }
+    for (int i = threadIdx.x; i < m * tail; i += kFewThreads) {
+      const int j = i / tail, c = whole * 16 + i - j * tail;
+      reinterpret_cast<int8_t*>(tokens)[static_cast<int64_t>(j) * kp * 16 + c] = x[j * ldx + c];
+    }
     if (threadIdx.x < m) token_scale[threadIdx.x] = p.sa[threadIdx.x];
   }
   __syncthreads();
 
   for (; channel < p.n; channel += step) {
-    int acc[kRows][kM] = {};
-    for (int at = 0; at < kp; at += 32 * kAhead) {
+    int acc[kM] = {};
+    if (lane < tail) {
+#pragma unroll
+      for (int j = 0; j < kM; ++j)
+        if (j < m) acc[j] = last * reinterpret_cast<const int8_t*>(tokens)[(j * kp + whole) * 16 + lane];
+    }
+    for (int at = 0; at < whole; at += 32 * kAhead) {
       if (at > 0) load(channel, at);
 #pragma unroll
       for (int i = 0; i < kAhead; ++i) {
         const int piece = at + lane + 32 * i;
-        if (piece < kp) {
+        if (piece < whole) {
 #pragma unroll
           for (int j = 0; j < kM; ++j) {
             if (j >= m) break;
             const int4 x = tokens[j * kp + piece];
-#pragma unroll
-            for (int r = 0; r < kRows; ++r)
-              acc[r][j] = __dp4a(w[r][i].w, x.w, __dp4a(w[r][i].z, x.z, __dp4a(w[r][i].y, x.y, __dp4a(w[r][i].x, x.x, acc[r][j]))));
+            acc[j] = __dp4a(w[i].w, x.w, __dp4a(w[i].z, x.z, __dp4a(w[i].y, x.y, __dp4a(w[i].x, x.x, acc[j]))));
           }
         }
       }
     }
-    load(channel + step, 0);
+    const float s = p.sb[channel], bias = p.bias ? p.bias[channel] : 0.0f;
+    if (channel + step < p.n) load(channel + step, 0);
+    int mine = 0;
 #pragma unroll
-    for (int r = 0; r < kRows; ++r) {
-      int mine = 0;
-#pragma unroll
-      for (int j = 0; j < kM; ++j) {
-        const int sum = __reduce_add_sync(0xffffffffu, acc[r][j]);
-        if (lane == j) mine = sum;
-      }
-      const int64_t c = channel + r;
-      if (lane < m && c < p.n)
-        put_output<kType>(p, lane, c, mine, token_scale[lane], p.sb[c], p.bias ? p.bias[c] : 0.0f);
+    for (int j = 0; j < kM; ++j) {
+      const int sum = __reduce_add_sync(0xffffffffu, acc[j]);
+      if (lane == j) mine = sum;
     }
+    if (lane < m) put_output<kType>(p, lane, channel, mine, token_scale[lane], s, bias);
   }
 }
 
@@ -630,20 +615,20 @@ cudaError_t int8_few_tokens(const void* X, int64_t ldx, const int8_t* B, int64_t
                             cudaStream_t st) {
   const size_t smem = static_cast<size_t>(p.m) * ((k + 15) / 16 * 16);
   const bool wide = kIn >= 0 && rows_aligned16(X, ldx, type_bytes(kIn));
-  const auto run = [&](auto kernel, int rows) {
+  const auto run = [&](auto kernel) {
     if (smem > 48 << 10) {
       const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kFewBytes));
       if (e != cudaSuccess) return e;
     }
-    const int64_t per = kFewThreads / 32 * rows, most = static_cast<int64_t>(sm_count()) * 4;
+    const int64_t per = kFewThreads / 32, most = static_cast<int64_t>(sm_count()) * 4;
     note_launch();
     return launch_kernel(kernel, dim3(static_cast<unsigned>(std::min((p.n + per - 1) / per, most))), kFewThreads, smem, st,
                          1, p.early, X, ldx, wide, B, ldb, p, k);
   };
-  if (p.m == 1) return run(k_int8_few<kIn, kType, 1>, 1);
-  if (p.m == 2) return run(k_int8_few<kIn, kType, 2>, 1);
-  if (p.m <= 4) return run(k_int8_few<kIn, kType, 4>, 2);
-  return run(k_int8_few<kIn, kType, 8>, 2);
+  if (p.m == 1) return run(k_int8_few<kIn, kType, 1>);
+  if (p.m == 2) return run(k_int8_few<kIn, kType, 2>);
+  if (p.m <= 4) return run(k_int8_few<kIn, kType, 4>);
+  return run(k_int8_few<kIn, kType, 8>);
 }
 
 bool few_tokens(int64_t m, int64_t k) { return m <= kFewTokens && m * ((k + 15) / 16 * 16) <= kFewBytes; }
