@@ -18,8 +18,9 @@ namespace {
 //
 // Two steps per row, a = max |x| and q = nearest(127 x / a). A row's kTPR threads
 // keep it in registers between the two (kKeep pieces of 8 entries each, as they lie in
-// memory), so X is read once; longer rows read the rest again, from L2. Bound by
-// memory: 3 bytes for a bfloat16 entry leave about 16 instructions for it.
+// memory), so X is read once; longer rows read the rest again, from L2. Between memory
+// and instruction issue: 3 bytes for a bfloat16 entry leave 16 instructions for it at
+// full bandwidth, and it takes 14 (16384 x 16384 bfloat16: 168 us, 4.8 TB/s, issue 64%).
 
 // A row's quantisation from its largest magnitude, given as the bits of a float.
 struct RowScale {
@@ -132,8 +133,11 @@ cudaError_t int8_rows(const void* X, int64_t n, int64_t k, int64_t ldx, int8_t* 
   const auto* x = static_cast<const typename Elem<kType>::T*>(X);
   const bool wide = rows_aligned16(X, ldx, type_bytes(kType));
   constexpr int kMost = kType == kF32 ? 4 : 8;  // 16384 16-bit or 8192 32-bit entries in registers
-  // a warp, four or eight of them per row; few rows take the most threads (latency)
-  if (k <= 1024 && n > 148) {
+  // A warp, four or eight of them per row: few rows take the most threads (latency),
+  // many rows the fewest. bfloat16, us with 1 / 4 / 8 warps: 100 x 1024 5.6 / - / 3.2,
+  // 1000 x 1024 5.8 / 4.5 / 8.7, 16384 x 1024 19 / 35 / 99, 1000 x 4096 - / 8.5 / 10.4,
+  // 16384 x 4096 175 (spills) / 70 / 118.
+  if (k <= 1024 && n > 2048) {
     k_int8_rows<kType, 32, 4, false>
         <<<static_cast<unsigned>((n + 3) / 4), 128, 0, st>>>(x, n, k, ldx, wide, Q, ldq, scale, status);
   } else if (k <= 4096 && n > 148) {
@@ -178,9 +182,10 @@ __device__ __forceinline__ void put_output(const Product& p, int64_t token, int6
       Elem<kType>::put(fmaf(static_cast<float>(acc) * a, s, bias));
 }
 
-// -- few tokens: a tile of 128 channels by kTok tokens per cluster, k split over the
+// -- up to 128 tokens: a tile of 128 channels by kTok tokens per cluster, k split over the
 // cluster's CTAs and joined through distributed shared memory (integers: the order
-// does not matter) --
+// does not matter). Bound by the loads into shared memory: 64 tokens by 16384 x 4096
+// weights take 26 us from DRAM (2.6 TB/s) and 15 us from L2. --
 
 template <int kTok>
 struct TileCfg {
@@ -343,7 +348,10 @@ cudaError_t int8_tile(const CUtensorMap& map_w, const CUtensorMap& map_x, const 
 
 // -- many tokens: a pair of CTAs (cta_group::2) per 256 channels by 256 tokens,
 // persistent over the tiles, the accumulators of one tile written out while the next
-// one is computed --
+// one is computed. Against the tiles above, with 4096 of k: 128 tokens by 4096 channels
+// 16.6 (tiles: 14.3) us, 256 by 4096 17.0 (19.5), 256 by 16384 18.7 (24.2), 512 by 4096
+// 17.4 (29.3). Bound by the tensor cores: 16384 tokens by 4096 channels by 16384 take
+// 597 us, 3.68 POP/s, with the tensor pipe busy 96% of the time. --
 
 constexpr int kPairStages = 6;
 constexpr int kPairThreads = 320;  // eight epilogue warps, the producer, the MMA issuer
@@ -499,12 +507,15 @@ cudaError_t int8_pair(const CUtensorMap& map_w, const CUtensorMap& map_x, const 
                        static_cast<int>(channel_tiles), static_cast<int>(token_tiles));
 }
 
-// -- up to 8 tokens: the weights' bytes are the cost, and one launch. Each CTA holds
-// all tokens in shared memory (quantising them itself when they come as floats) and
-// its warps take output channels in turn, a lane 16 bytes of k at a time (dp4a). The
-// first channels' weights are on their way while the tokens are quantised. --
+// -- one or two tokens: the weights' bytes are the cost, and set-up time. Each CTA holds
+// the tokens in shared memory (quantising them itself when they come as floats) and its
+// warps take output channels in turn, a lane 16 bytes of k at a time (dp4a). The first
+// channels' weights are on their way while the tokens are. Without barriers, TMEM and a
+// join it beats the tensor-core tiles below for 4096 x 4096 weights in L2: 3.9 against
+// 6.2 us for one token, 4.9 against 6.3 for two; at four (9.0 against 6.4) each token's
+// reads of shared memory cost more than they. Bound by latency: 16.8 MB in 3.9 us. --
 
-constexpr int kFewTokens = 8;
+constexpr int kFewTokens = 2;
 constexpr int64_t kFewBytes = 64 << 10;  // shared memory of the tokens
 constexpr int kFewThreads = 256;
 
@@ -625,17 +636,15 @@ cudaError_t int8_few_tokens(const void* X, int64_t ldx, const int8_t* B, int64_t
     return launch_kernel(kernel, dim3(static_cast<unsigned>(std::min((p.n + per - 1) / per, most))), kFewThreads, smem, st,
                          1, p.early, X, ldx, wide, B, ldb, p, k);
   };
-  if (p.m == 1) return run(k_int8_few<kIn, kType, 1>);
-  if (p.m == 2) return run(k_int8_few<kIn, kType, 2>);
-  if (p.m <= 4) return run(k_int8_few<kIn, kType, 4>);
-  return run(k_int8_few<kIn, kType, 8>);
+  return p.m == 1 ? run(k_int8_few<kIn, kType, 1>) : run(k_int8_few<kIn, kType, 2>);
 }
 
 bool few_tokens(int64_t m, int64_t k) { return m <= kFewTokens && m * ((k + 15) / 16 * 16) <= kFewBytes; }
-// Whether each CTA quantises the tokens itself: that repeats the work in every CTA, and
-// a second launch is cheaper for more entries (7 tokens of 4099 float32 entries: 26 us
-// in one kernel).
-bool few_entries(int64_t m, int64_t k) { return few_tokens(m, k) && m * k <= 8192; }
+// Whether each CTA quantises the tokens itself. That repeats the work in every CTA: one
+// token of 4096 bfloat16 entries takes 7.3 us so and 6.5 us as two launches, but a second
+// launch costs the host 2 us more than that; at 8192 entries it is 11.0 against 8.7, at
+// two tokens of 4096 10.0 against 7.2.
+bool few_entries(int64_t m, int64_t k) { return few_tokens(m, k) && m * k <= 4096; }
 
 // A map of 8-bit rows in boxes of 128 bytes by `rows`.
 bool map_rows8(CUtensorMap* map, const int8_t* p, int64_t n, int64_t k, int64_t ld, int rows) {
@@ -665,7 +674,7 @@ cudaError_t int8_product(const int8_t* A, int64_t lda, const int8_t* B, int64_t 
   if (p.m <= 16) return int8_split<kType, 16>(A, lda, B, ldb, p, k, st);
   if (p.m <= 32) return int8_split<kType, 32>(A, lda, B, ldb, p, k, st);
   if (p.m <= 64) return int8_split<kType, 64>(A, lda, B, ldb, p, k, st);
-  if (p.m <= 256) return int8_split<kType, 128>(A, lda, B, ldb, p, k, st);
+  if (p.m <= 128) return int8_split<kType, 128>(A, lda, B, ldb, p, k, st);
   CUtensorMap map_w, map_x;
   if (!map_rows8(&map_w, B, p.n, k, ldb, 128) || !map_rows8(&map_x, A, p.m, k, lda, 128)) return cudaErrorInvalidValue;
   return int8_pair<kType>(map_w, map_x, p, st);
