@@ -558,7 +558,8 @@ __global__ void __launch_bounds__(256)
 }
 
 // How a gradient is cut: the token axis into as many parts as leave pairs idle otherwise, of
-// at least 8 pieces (65536 tokens, 512 x 512: 18 parts, 34 us and 7 us for the join);
+// at least 4 pieces (512 x 512, us in one part and split: 65536 tokens 322 and 39, 4096
+// tokens 31 and 18, where parts of at least 8 pieces took 20; 1024 tokens 16 and 16);
 // bf16 terms and whether dY is copied into them; the workspace.
 struct GradientPlan {
   int terms, split, per;
@@ -575,7 +576,7 @@ GradientPlan gradient_plan(const void* dY, int64_t t, int64_t o, int64_t k, int 
   const int64_t pieces = (t + kTok - 1) / kTok, tiles = ((o + 255) / 256) * ((k + 255) / 256);
   const int64_t pairs = sm_count() / 2;
   int64_t split = tiles < pairs ? pairs / tiles : 1;
-  split = std::max<int64_t>(1, std::min(split, pieces / 8));
+  split = std::max<int64_t>(1, std::min(split, pieces / 4));
   p.per = static_cast<int>((pieces + split - 1) / split);
   p.split = static_cast<int>((pieces + p.per - 1) / p.per);
   p.terms_bytes = p.copy ? (static_cast<size_t>(p.terms) * t * p.ld * 2 + 255) / 256 * 256 : 0;

@@ -185,7 +185,7 @@ __device__ __forceinline__ void put_output(const Product& p, int64_t token, int6
 // -- up to 128 tokens: a tile of 128 channels by kTok tokens per cluster, k split over the
 // cluster's CTAs and joined through distributed shared memory (integers: the order
 // does not matter). Bound by the loads into shared memory: 64 tokens by 16384 x 4096
-// weights take 26 us from DRAM (2.6 TB/s) and 15 us from L2. --
+// weights take 12.5 us from L2 (67 MB, 5.4 TB/s). --
 
 template <int kTok>
 struct TileCfg {
@@ -316,11 +316,20 @@ __global__ void __launch_bounds__(192, 2)
       const int tokens = static_cast<int>(min(static_cast<int64_t>(kTok), p.m - token0));
       if (channel < p.n) {
         const float s = p.sb[channel], bias = p.bias ? p.bias[channel] : 0.0f;
-        for (int j = part; j < tokens; j += split) {
-          int sum = 0;
-          for (int r = 0; r < split; ++r)
-            sum += ld_shared_cluster(map_shared(tiles + 4 * (j * 128 + warp * 32 + lane), r));
-          put_output<kType>(p, token0 + j, channel, sum, __ldg(p.sa + token0 + j), s, bias);
+        constexpr int kAtOnce = 8;  // tokens of this CTA's share whose partial sums are in flight
+        for (int j0 = part; j0 < tokens; j0 += split * kAtOnce) {
+          int sum[kAtOnce] = {};
+          for (int r = 0; r < split; ++r) {
+            const uint32_t from = map_shared(tiles + 4 * (warp * 32 + lane), r);
+#pragma unroll
+            for (int u = 0; u < kAtOnce; ++u)
+              if (j0 + u * split < tokens) sum[u] += ld_shared_cluster(from + 512 * (j0 + u * split));
+          }
+#pragma unroll
+          for (int u = 0; u < kAtOnce; ++u) {
+            const int j = j0 + u * split;
+            if (j < tokens) put_output<kType>(p, token0 + j, channel, sum[u], __ldg(p.sa + token0 + j), s, bias);
+          }
         }
       }
     }
@@ -349,7 +358,7 @@ cudaError_t int8_tile(const CUtensorMap& map_w, const CUtensorMap& map_x, const 
 // -- many tokens: a pair of CTAs (cta_group::2) per 256 channels by 256 tokens,
 // persistent over the tiles, the accumulators of one tile written out while the next
 // one is computed. Against the tiles above, with 4096 of k: 128 tokens by 4096 channels
-// 16.6 (tiles: 14.3) us, 256 by 4096 17.0 (19.5), 256 by 16384 18.7 (24.2), 512 by 4096
+// 16.6 (tiles: 13.8) us, 256 by 4096 17.0 (19.5), 256 by 16384 18.7 (24.2), 512 by 4096
 // 17.4 (29.3). Bound by the tensor cores: 16384 tokens by 4096 channels by 16384 take
 // 597 us, 3.68 POP/s, with the tensor pipe busy 96% of the time. --
 
@@ -660,9 +669,11 @@ cudaError_t int8_split(const int8_t* A, int64_t lda, const int8_t* B, int64_t ld
   if (!map_rows8(&map_w, B, p.n, k, ldb, 128) || !map_rows8(&map_x, A, p.m, k, lda, kTok)) return cudaErrorInvalidValue;
   const int64_t tiles = (p.n + 127) / 128 * ((p.m + kTok - 1) / kTok);
   if (tiles > INT32_MAX / 16) return cudaErrorInvalidValue;
-  // split k until the CTAs fill the GPU (two per SM), with at least two pieces each
+  // Split k while the CTAs leave SMs idle, with at least two pieces each. us with 1 / 2 / 4
+  // / 8 parts: 16 tokens by 4096 x 4096 8.4 / 7.2 / 6.4 / 8.0, 128 by 4096 x 4096 17.3 / 16.8
+  // / 13.8 / 15.1; 64 by 16384 x 4096 12.5 / 13.9 (a second CTA per SM shares its loads).
   int split = 1;
-  while (split < 8 && tiles * split * 2 <= 2 * sm_count() && p.pieces >= 4 * split) split *= 2;
+  while (split < 8 && tiles * split * 2 <= sm_count() && p.pieces >= 4 * split) split *= 2;
   while (split > 1 && (split - 1) * ((p.pieces + split - 1) / split) >= p.pieces) split /= 2;
   return int8_tile<kType, kTok>(map_w, map_x, p, split, st);
 }
