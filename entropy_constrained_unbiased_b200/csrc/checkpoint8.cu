@@ -175,16 +175,16 @@ void piece_grid(int64_t t, int64_t pieces, dim3* grid, dim3* block) {
 // adjacent entries of a row of dW. A pair of CTAs (cta_group::2) takes 256 features
 // by 256 outputs; each CTA converts its own 128 features only.
 //
-// Bound by the tensor cores and their clock (16384 tokens, 4096 x 4096, bfloat16: 396 us,
-// 1.39 PFLOP/s, tensor pipe 73% at 1.58 GHz; the 256 tiles are 3.46 rounds of 74 pairs).
+// Bound by the tensor cores and their clock (16384 tokens, 4096 x 4096, bfloat16: 420 us,
+// 1.31 PFLOP/s; the 256 tiles are 3.46 rounds of 74 pairs).
 // float32 dY, 4096 tokens, 4096 x 1024: 70 us behind 30 us for its terms.
 //
 // The tensor core adds to its float32 accumulator by cutting, not rounding: a step of
-// 16 tokens loses up to 2^-23 of the running sum, always towards zero, and n steps
-// about 2.3e-8 n of it (measured: 2.2e-6 after 96). That is far below a bfloat16
-// result's own rounding (2^-9 on average), and one accumulator takes the whole sum. For float32
-// and float16 results (kExact) an accumulator takes 16 steps or so, and the epilogue
-// warps add it, rounding to nearest, to sums that they hold in registers.
+// 16 tokens loses up to 2^-23 of the running sum, always towards zero (measured: 2.2e-6
+// after 96 steps of random signs, 7.1e-4 after 8192 steps of positive products). So an accumulator takes a few steps only and
+// the epilogue warps add it, rounding to nearest, to sums that they hold in registers:
+// 16 steps (24 for the three terms of a float32 dY) for float32 and float16 results, 64
+// for bfloat16 results (at most 2^-17 of the sum, against 2^-8 for their own rounding).
 
 __device__ int g_stalled_checkpoint8;  // set when a bounded wait gave up
 
@@ -199,21 +199,23 @@ constexpr int kQStage = kInts + kScales;
 constexpr int kQStages = 7, kXStages = 4, kYStages = 6;
 constexpr int kGradSmem = kQStages * kQStage + kXStages * kOperand + kYStages * kOperand + 1024;
 
-// Warps: the epilogue's, the producers of dY and of the integers, the MMA issuer, the
-// converters. The converters
+// Warps: the epilogue's, the producers of dY and of the integers, the MMA issuer, an
+// idle one, the converters. The converters
 // come in kXStages groups that take the stages in turn, so that the latencies of one
 // stage's conversion (its wait, its loads, the fence, the arrival at the other CTA)
-// are covered by three others'. kExact holds 128 sums a thread in the epilogue's
-// registers, so its warps come in groups of four that trade registers (setmaxnreg):
-// 256 * 184 + 256 * 72 = 512 * 128.
-template <bool kExact>
-struct GradWarps {
-  static constexpr int kEpilogue = kExact ? 8 : 4;
-  static constexpr int kLoad = kEpilogue, kIssue = kEpilogue + 1, kLoadInts = kEpilogue + 2;
-  static constexpr int kConvert0 = kExact ? 12 : 7;
-  static constexpr int kConvert = kExact ? 4 : 16;
-  static constexpr int kThreads = 32 * (kConvert0 + kConvert);
-};
+// are covered by three others'. The epilogue's threads hold 128 sums each, so the warps
+// come in groups of four that trade registers (setmaxnreg): of the launch's 896 * 72 =
+// 64512 they take 256 * 168 + 640 * 32 = 63488. 16384 x 4096 x 4096, us, with 4 / 8 / 16
+// converters: 538 / 441 / 420.
+constexpr int kEpilogue = 8;
+constexpr int kLoad = 8, kIssue = 9, kLoadInts = 10;
+constexpr int kConvert0 = 12, kConvert = 16;
+constexpr int kGradThreads = 32 * (kConvert0 + kConvert);
+constexpr int kLaunchRegisters = 72;  // 65536 / 896 in steps of 8: what __launch_bounds__ gives a thread
+constexpr int kMostRegisters = 168, kFewRegisters = 32;
+static_assert(32 * kEpilogue * kMostRegisters + (kGradThreads - 32 * kEpilogue) * kFewRegisters <=
+                  kGradThreads * kLaunchRegisters,
+              "the warps wait for ever for registers that the block was not launched with");
 
 struct Gradient {
   void* out;          // dW, or the partial sums when the tokens are split
@@ -251,11 +253,10 @@ __device__ __forceinline__ uint32_t ld_shared1(uint32_t addr) {
   return v;
 }
 
-template <int kOut, bool kExact>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GradWarps<kExact>::kThreads, 1)
+template <int kOut>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGradThreads, 1)
     k_wgrad(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_s,
             const __grid_constant__ CUtensorMap map_y, const Gradient g) {
-  using W = GradWarps<kExact>;
   extern __shared__ unsigned char smem_raw[];
   __shared__ uint64_t bars[2 * kQStages + 2 * kXStages + 2 * kYStages + 4];
   __shared__ uint32_t tmem_slot;
@@ -266,7 +267,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GradWarps<kExact>::k
   const uint32_t ints = smem_addr(bars), q_empty = ints + 8 * kQStages, ready = q_empty + 8 * kQStages,
                  x_empty = ready + 8 * kXStages, full = x_empty + 8 * kXStages, y_empty = full + 8 * kYStages,
                  done = y_empty + 8 * kYStages, freed = done + 16;
-  constexpr int kGroup = W::kConvert / kXStages;  // warps that convert one stage
+  constexpr int kGroup = kConvert / kXStages;  // warps that convert one stage
   const int warp = __shfl_sync(0xffffffffu, warp_id(), 0), lane = lane_id();
   const int rank = static_cast<int>(cluster_rank());
   const int pair = static_cast<int>(blockIdx.x) >> 1, pairs = static_cast<int>(gridDim.x) >> 1;
@@ -274,7 +275,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GradWarps<kExact>::k
   const int all = tiles * g.split;
   next_may_begin();
 
-  if (warp == W::kLoad) tmem_alloc<2>(smem_addr(&tmem_slot), 512);
+  if (warp == kLoad) tmem_alloc<2>(smem_addr(&tmem_slot), 512);
   if (threadIdx.x == 0) {
     prefetch_map(&map_q);
     prefetch_map(&map_s);
@@ -293,7 +294,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GradWarps<kExact>::k
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(done + 8 * i, 1);
-      mbar_init(freed + 8 * i, 2 * W::kEpilogue);
+      mbar_init(freed + 8 * i, 2 * kEpilogue);
     }
     fence_mbar_init();
   }
@@ -303,9 +304,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GradWarps<kExact>::k
   const uint32_t acc = __shfl_sync(0xffffffffu, tmem_slot, 0);
   bool ok = true;
 
-  if (warp >= W::kEpilogue) {
-    if constexpr (kExact) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
-    if (warp == W::kLoad) {
+  if (warp >= kEpilogue) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kFewRegisters));
+    if (warp == kLoad) {
       const bool elected = elect_one();
       const uint32_t full0 = map_shared(full, 0);
       after_previous();  // dY's terms; the integers do not wait for them
@@ -327,7 +328,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GradWarps<kExact>::k
           }
       }
       if (!ok && rank == 0) y.drain(full, kWaitLimit);  // before the memory is given back
-    } else if (warp == W::kLoadInts) {
+    } else if (warp == kLoadInts) {
       const bool elected = elect_one();
       Ring<kQStages> q;
       for (int w = pair; w < all && ok; w += pairs) {
@@ -346,7 +347,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GradWarps<kExact>::k
         }
       }
       if (!ok) q.drain(ints, kWaitLimit);
-    } else if (warp == W::kIssue && rank == 0) {
+    } else if (warp == kIssue && rank == 0) {
       const bool elected = elect_one();
       Ring<kXStages> x;
       Ring<kYStages> y;
@@ -381,11 +382,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GradWarps<kExact>::k
           if (elected) mma_commit<2>(done + 8 * out.stage);
         }
       }
-    } else if (warp >= W::kConvert0) {
+    } else if (warp >= kConvert0) {
       constexpr int kRows = kTok / kGroup;  // tokens of one warp
       const uint32_t ready0 = map_shared(ready, 0);
-      const uint32_t group = (warp - W::kConvert0) / kGroup;  // and the X^ stage that it fills
-      const int row = (warp - W::kConvert0) % kGroup * kRows + (lane >> 3), chunk = lane & 7;
+      const uint32_t group = (warp - kConvert0) / kGroup;  // and the X^ stage that it fills
+      const int row = (warp - kConvert0) % kGroup * kRows + (lane >> 3), chunk = lane & 7;
       // 16-byte pieces 2c and 2c + 1 of a 128-byte row, swizzled by the row; the upper 64
       // features write theirs in the other order, so that the eight threads of a row
       // hit different banks
@@ -404,7 +405,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GradWarps<kExact>::k
           if (!ok) break;
           const uint32_t from = qs + q.stage * kQStage + row * 128 + chunk * 16;
           const uint32_t scales = qs + q.stage * kQStage + kInts + row * 16 + block;
-#pragma unroll 4
+#pragma unroll 2
           for (int r = 0; r < kRows; r += 4) {
             const uint4 x = ld_shared16(from + r * 128);
             const uint32_t b = ld_shared1(scales + r * 16);
@@ -428,9 +429,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GradWarps<kExact>::k
       }
     }
   } else {
-    if constexpr (kExact) asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
-    constexpr int kCols = kExact ? 128 : 256;  // columns of this warp
-    const int col0 = kExact ? (warp >> 2) * 128 : 0;
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kMostRegisters));
+    constexpr int kCols = 128;  // columns of this warp
+    const int col0 = (warp >> 2) * 128;
     const uint32_t lanes = acc + (static_cast<uint32_t>(warp & 3) << 21) + col0;
     const uint32_t freed0 = map_shared(freed, 0);
     int n = 0;
@@ -441,51 +442,30 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GradWarps<kExact>::k
       const int rows = static_cast<int>(min(static_cast<int64_t>(kCols), g.o - o0));  // may be 0 or less
       auto* out = static_cast<typename Elem<kOut>::T*>(g.out) + (part * g.o + o0) * g.ld + feature;
       const int count = min(g.pieces, (part + 1) * g.per) - part * g.per;
-      if constexpr (kExact) {
-        float sum[kCols];
+      float sum[kCols];
 #pragma unroll
-        for (int j = 0; j < kCols; ++j) sum[j] = 0.0f;
-        for (int i = 0; i < count; i += g.chunk, ++n) {
-          const int buf = n & 1;
-          ok = __all_sync(0xffffffffu, mbar_wait_bounded(done + 8 * buf, (n >> 1) & 1, kWaitLimit));
-          if (!ok) break;
-          tcgen05_after_sync();
-#pragma unroll
-          for (int j0 = 0; j0 < kCols; j0 += 16) {
-            uint32_t v[16];
-            tmem_ld16(lanes + buf * 256 + j0, v);
-            tcgen05_wait_ld();
-#pragma unroll
-            for (int j = 0; j < 16; ++j) sum[j0 + j] += __uint_as_float(v[j]);
-          }
-          tcgen05_before_sync();
-          __syncwarp();
-          if (lane == 0) mbar_arrive_cluster(freed0 + 8 * buf);
-        }
-        if (ok && feature < g.k) {
-#pragma unroll
-          for (int j = 0; j < kCols; ++j)
-            if (j < rows) out[j * g.ld] = Elem<kOut>::put(sum[j]);
-        }
-      } else {
+      for (int j = 0; j < kCols; ++j) sum[j] = 0.0f;
+      for (int i = 0; i < count; i += g.chunk, ++n) {
         const int buf = n & 1;
-        ++n;
-        ok = __all_sync(0xffffffffu, mbar_wait_bounded(done + 8 * buf, ((n - 1) >> 1) & 1, kWaitLimit));
+        ok = __all_sync(0xffffffffu, mbar_wait_bounded(done + 8 * buf, (n >> 1) & 1, kWaitLimit));
         if (!ok) break;
         tcgen05_after_sync();
-        for (int j0 = 0; j0 < rows; j0 += 32) {
-          uint32_t v[32];
-          tmem_ld32(lanes + buf * 256 + j0, v);
-          tcgen05_wait_ld();
-          if (feature < g.k) {
 #pragma unroll
-            for (int j = 0; j < 32; ++j)
-              if (j0 + j < rows) out[(j0 + j) * g.ld] = Elem<kOut>::put(__uint_as_float(v[j]));
-          }
+        for (int j0 = 0; j0 < kCols; j0 += 16) {
+          uint32_t v[16];
+          tmem_ld16(lanes + buf * 256 + j0, v);
+          tcgen05_wait_ld();
+#pragma unroll
+          for (int j = 0; j < 16; ++j) sum[j0 + j] += __uint_as_float(v[j]);
         }
         tcgen05_before_sync();
         __syncwarp();
         if (lane == 0) mbar_arrive_cluster(freed0 + 8 * buf);
+      }
+      if (ok && feature < g.k) {
+#pragma unroll
+        for (int j = 0; j < kCols; ++j)
+          if (j < rows) out[j * g.ld] = Elem<kOut>::put(sum[j]);
       }
     }
   }
@@ -493,7 +473,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GradWarps<kExact>::k
   __syncwarp();
   tcgen05_before_sync();
   cluster_sync_all();  // neither CTA leaves while the other's MMAs or copies use its memory
-  if (warp == W::kLoad) {
+  if (warp == kLoad) {
     tcgen05_after_sync();
     tmem_free<2>(acc, 512);
   }
@@ -593,32 +573,38 @@ void split_terms(const void* dY, int64_t ldy, int64_t t, int64_t o, __nv_bfloat1
   note_launch();
 }
 
-template <int kOut, bool kExact>
+template <int kOut>
 cudaError_t wgrad(const CUtensorMap& map_q, const CUtensorMap& map_s, const CUtensorMap& map_y, const Gradient& g,
                   cudaStream_t st) {
-  const cudaError_t e = cudaFuncSetAttribute(k_wgrad<kOut, kExact>, cudaFuncAttributeMaxDynamicSharedMemorySize, kGradSmem);
+  // setmaxnreg waits for ever if the compiler gave the launch fewer registers than its split hands out
+  static const bool enough = [] {
+    cudaFuncAttributes a;
+    return cudaFuncGetAttributes(&a, k_wgrad<kOut>) == cudaSuccess && a.numRegs == kLaunchRegisters;
+  }();
+  if (!enough) return cudaErrorInvalidConfiguration;
+  const cudaError_t e = cudaFuncSetAttribute(k_wgrad<kOut>, cudaFuncAttributeMaxDynamicSharedMemorySize, kGradSmem);
   if (e != cudaSuccess) return e;
   const int64_t all = static_cast<int64_t>(g.feature_tiles) * g.output_tiles * g.split;
   const int pairs = static_cast<int>(std::min<int64_t>(sm_count() / 2, all));
   note_launch();
-  return launch_kernel(k_wgrad<kOut, kExact>, dim3(2 * pairs), GradWarps<kExact>::kThreads, kGradSmem, st, 1, g.early,
+  return launch_kernel(k_wgrad<kOut>, dim3(2 * pairs), kGradThreads, kGradSmem, st, 1, g.early,
                        map_q, map_s, map_y, g);
 }
 
 template <int kOut>
 cudaError_t wgrad_all(const CUtensorMap& map_q, const CUtensorMap& map_s, const CUtensorMap& map_y, Gradient g,
                       float* part, void* dW, int64_t ldw, cudaStream_t st) {
-  constexpr bool kExact = kOut != kBF16;
-  // 16 steps of 16 tokens per accumulator, where the terms after the first piece's smaller ones count as steps too
-  g.chunk = !kExact ? g.per : (g.terms == 1 ? 4 : 2);
+  // Pieces of four steps for each term of dY. bfloat16 results of 16384 x 4096 x 4096 take
+  // 449 / 431 / 420 / 416 us with 4 / 8 / 16 / 32 pieces (398 with one accumulator for all).
+  g.chunk = kOut == kBF16 ? 16 / g.terms : (g.terms == 1 ? 4 : 2);
   if (g.split == 1) {
     g.out = dW;
     g.ld = ldw;
-    return wgrad<kOut, kExact>(map_q, map_s, map_y, g, st);
+    return wgrad<kOut>(map_q, map_s, map_y, g, st);
   }
   g.out = part;
   g.ld = g.k;
-  const cudaError_t e = wgrad<kF32, kExact>(map_q, map_s, map_y, g, st);
+  const cudaError_t e = wgrad<kF32>(map_q, map_s, map_y, g, st);
   if (e != cudaSuccess) return e;
   note_launch();
   return launch_kernel(k_join<kOut>, column_grid(g.o, g.k), 256, 0, st, 1, true, part, g.split, g.o, g.k, static_cast<typename Elem<kOut>::T*>(dW), ldw);

@@ -169,6 +169,24 @@ def test_weight_gradient_same_sign(E, dtype):
     assert np.linalg.norm(_f64(dW) - ref) <= 2e-6 * np.linalg.norm(ref)
 
 
+def test_weight_gradient_long_sums_are_not_cut(E):
+    """131072 positive products per entry: the sums do not drift towards zero. With outputs spread evenly over a binade
+    the results' own roundings cancel in the mean: what stays of it is 5 standard errors of 2^-8 / 3^(1/2) each and
+    2^-16 at the binade's ends. An accumulator may lose 2^-23 for each of its 64 steps, and each of the 128 that are
+    joined adds a rounding of at most 2^-24."""
+    t, o, k = 131072, 1792, 1536  # 42 tiles: the tokens are not split
+    g = torch.Generator("cuda").manual_seed(1)
+    q, b = E.checkpoint8(torch.rand((t, k), generator=g, device="cuda").bfloat16(), 5)
+    dY = (torch.rand((t, o), generator=g, device="cuda") * (1 + torch.arange(o, device="cuda") / o)).bfloat16()
+    ref = torch.zeros((o, k), dtype=torch.float64, device="cuda")
+    for r in range(0, t, 16384):
+        ref += dY[r : r + 16384].double().T @ E.checkpoint8_restore(q[r : r + 16384], b[r : r + 16384]).double()
+    drift = (E.checkpoint8_wgrad(dY, q, b).double() - ref).sum() / ref.sum()
+    assert abs(float(drift)) <= 64 * 2.0**-23 + 128 * 2.0**-24 + 5 * 2.0**-8 / 3**0.5 / (o * k) ** 0.5 + 2.0**-16
+    drift = (E.checkpoint8_wgrad(dY, q, b, torch.float32).double() - ref).sum() / ref.sum()
+    assert abs(float(drift)) <= 16 * 2.0**-23 + 512 * 2.0**-24
+
+
 def test_weight_gradient_no_tokens(E):
     q, b = E.checkpoint8(torch.empty((0, 70), device="cuda"), 1)
     dW = E.checkpoint8_wgrad(torch.empty((0, 50), device="cuda"), q, b)
