@@ -4,6 +4,10 @@ The quantiser is compared for equality (the integers follow from the exact
 quotient, the scale is one float32 division). The product's integer sum is
 exact, so an output may be off by four float32 roundings (the conversion of the
 sum, two scales, the bias) of at most 2^-24 each, and one of the output type."""
+import os
+import subprocess
+import sys
+
 import numpy as np
 import pytest
 import torch
@@ -233,3 +237,32 @@ def test_overlapping_calls_and_graph_replay(E):
             g.replay()
         torch.cuda.synchronize()
         assert torch.equal(y, int8_linear(x, wq, ws))
+
+
+LONG_FEW = """
+import torch
+from entropy_constrained_unbiased_b200 import ecasq as E
+
+for m, k in [(1, 49137), (1, 49152), (2, 24561), (2, 24576), (1, 49153), (1, 65536), (2, 32768)]:
+    g = torch.Generator().manual_seed(k)
+    rows = torch.zeros((m + 20, (k + 31) // 32 * 32), dtype=torch.int8)
+    rows[:, :k] = torch.randint(-127, 128, (m + 20, k), generator=g, dtype=torch.int8)
+    rows = rows.cuda()[:, :k]
+    A, B, ones = rows[:m], rows[m:], torch.ones(20, device="cuda")
+    want = (A.double() @ B.double().T).float()
+    for dtype in (torch.float32, torch.bfloat16, torch.float16):
+        scale = torch.full((m,), 2.0**-16, device="cuda")
+        assert torch.equal(E.int8_matmul(A, scale, B, ones, None, dtype), (want * 2.0**-16).to(dtype)), (m, k, dtype)
+        x = A.to(dtype)
+        x[:, 0] = 127
+        q, s, _ = E.int8_quantize(x)
+        assert torch.equal(E.int8_linear(x, B, ones), E.int8_matmul(q, s, B, ones, None, dtype)), (m, k, dtype)
+"""
+
+
+def test_few_tokens_around_48_kb():
+    """Tokens that need 48 KB of shared memory, just less and more, in a process whose first calls they are (a longer
+    call before them would have raised the kernel's limit)."""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    run = subprocess.run([sys.executable, "-c", LONG_FEW], cwd=root, capture_output=True, text=True, timeout=300)
+    assert run.returncode == 0, run.stderr[-2000:]
