@@ -566,7 +566,7 @@ int ecasq_checkpoint8_wgrad(const void* dY, int dy_type, int64_t ldy, const int8
   if (!dW || !valid_pitch(o, k, ldw)) return ECASQ_ERR_ARG;
   if (t > 0 && (!dY || !valid_pitch(t, o, ldy) || !valid_checkpoint(q, ldq, scale, lds, k))) return ECASQ_ERR_ARG;
   const size_t need = checkpoint8_wgrad_workspace(dY, dy_type, ldy, t, o, k);
-  if (need && (!ws || ws_bytes < need)) return ECASQ_ERR_WORKSPACE;
+  if (need && (!ws || ws_bytes < need || (reinterpret_cast<uintptr_t>(ws) & 15) != 0)) return ECASQ_ERR_WORKSPACE;
   return cuda_status(launch_checkpoint8_wgrad(dY, dy_type, ldy, q, ldq, scale, lds, t, o, k, dW, dw_type, ldw, ws,
                                               static_cast<cudaStream_t>(stream)));
 }

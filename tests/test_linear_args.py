@@ -85,6 +85,17 @@ def test_gradient_arguments(lib):
     assert size(P16, 1, 64, -1, 64, 100) == 0 and size(P16, 1, 64, 4, 0, 100) == 0 and size(P16, 9, 64, 4, 64, 100) == 0
 
 
+def test_gradient_workspace(lib):
+    """Null, short and misaligned workspaces are refused: dY is copied into bf16 terms (float16, float32, rows off the
+    16-byte boundary), or the sum over the tokens is split."""
+    f, size = lib.ecasq_checkpoint8_wgrad, lib.ecasq_checkpoint8_wgrad_workspace_size
+    for ty, ldy, t in [(0, 64, 4), (2, 64, 4), (1, 65, 4), (1, 64, 4096)]:
+        need = size(P16, ty, ldy, t, 64, 100)
+        assert need > 0
+        for ws, have in [(NULL, need), (P16, need - 1), (ODD, need), (C.c_void_p(P16.value + 2), need)]:
+            assert f(P16, ty, ldy, P16, 128, P16, 16, t, 64, 100, P16, 1, 100, ws, have, NULL) == -3, (ty, ldy, t, ws, have)
+
+
 def test_no_cpu_path():
     from entropy_constrained_unbiased_b200 import ecasq as E
     from entropy_constrained_unbiased_b200.linear import checkpoint_linear, int8_linear
