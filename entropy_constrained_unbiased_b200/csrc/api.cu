@@ -83,6 +83,10 @@ constexpr int64_t kMaxCols8 = int64_t(1) << 26;
 constexpr int64_t kMaxK8 = 131072;  // 127^2 * 131072 < 2^31
 
 bool valid_type(int type) { return type == ECASQ_F32 || type == ECASQ_BF16 || type == ECASQ_F16; }
+// An array of the given type, on an element boundary.
+bool valid_array(const void* p, int type) {
+  return p && reinterpret_cast<uintptr_t>(p) % (type == ECASQ_F32 ? 4 : 2) == 0;
+}
 bool valid_rows(int64_t n, int64_t k) { return n >= 0 && n <= kMaxRows8 && k >= 1 && k <= kMaxCols8; }
 // A matrix of n rows with pitch ld: the pitch of a single row says nothing.
 bool valid_pitch(int64_t n, int64_t k, int64_t ld) { return n <= 1 || ld >= k; }
@@ -501,7 +505,7 @@ int ecasq_int8_quantize(const void* X, int x_type, int64_t n, int64_t k, int64_t
                         float* scale, int32_t* status, void* stream) {
   if (!valid_type(x_type) || !valid_rows(n, k)) return ECASQ_ERR_ARG;
   if (n == 0) return ECASQ_OK;
-  if (!X || !valid_pitch(n, k, ldx) || !valid_bytes(q, k, ldq, 16) || !scale || !status) return ECASQ_ERR_ARG;
+  if (!valid_array(X, x_type) || !valid_pitch(n, k, ldx) || !valid_bytes(q, k, ldq, 16) || !scale || !status) return ECASQ_ERR_ARG;
   return cuda_status(
       launch_int8_quantize(X, x_type, n, k, ldx, q, ldq, scale, status, static_cast<cudaStream_t>(stream)));
 }
@@ -511,7 +515,8 @@ int ecasq_int8_matmul(const int8_t* A, int64_t lda, const float* sa, const int8_
                       void* stream) {
   if (!valid_type(y_type) || !valid_rows(m, k) || n < 1 || n > kMaxRows8 || k > kMaxK8) return ECASQ_ERR_ARG;
   if (m == 0) return ECASQ_OK;
-  if (!valid_bytes(A, k, lda, 16) || !valid_bytes(B, k, ldb, 16) || !sa || !sb || !Y || !valid_pitch(m, n, ldy))
+  if (!valid_bytes(A, k, lda, 16) || !valid_bytes(B, k, ldb, 16) || !sa || !sb || !valid_array(Y, y_type) ||
+      !valid_pitch(m, n, ldy))
     return ECASQ_ERR_ARG;
   return cuda_status(launch_int8_matmul(A, lda, sa, B, ldb, sb, bias, m, n, k, Y, y_type, ldy,
                                         static_cast<cudaStream_t>(stream)));
@@ -526,7 +531,8 @@ int ecasq_int8_linear(const void* X, int x_type, int64_t ldx, const int8_t* B, i
                       size_t ws_bytes, void* stream) {
   if (!valid_type(x_type) || !valid_rows(m, k) || n < 1 || n > kMaxRows8 || k > kMaxK8) return ECASQ_ERR_ARG;
   if (m == 0) return ECASQ_OK;
-  if (!X || !valid_pitch(m, k, ldx) || !valid_bytes(B, k, ldb, 16) || !sb || !Y || !valid_pitch(m, n, ldy))
+  if (!valid_array(X, x_type) || !valid_pitch(m, k, ldx) || !valid_bytes(B, k, ldb, 16) || !sb ||
+      !valid_array(Y, x_type) || !valid_pitch(m, n, ldy))
     return ECASQ_ERR_ARG;
   const size_t need = int8_linear_workspace(m, k);
   if (need && (!ws || ws_bytes < need || (reinterpret_cast<uintptr_t>(ws) & 15) != 0)) return ECASQ_ERR_WORKSPACE;
@@ -538,7 +544,8 @@ int ecasq_checkpoint8(const void* X, int x_type, int64_t t, int64_t k, int64_t l
                       const uint64_t* seed_add, int8_t* q, int64_t ldq, uint8_t* scale, int64_t lds, void* stream) {
   if (!valid_type(x_type) || !valid_rows(t, k)) return ECASQ_ERR_ARG;
   if (t == 0) return ECASQ_OK;
-  if (!X || !valid_pitch(t, k, ldx) || !valid_checkpoint(q, ldq, scale, lds, k)) return ECASQ_ERR_ARG;
+  if (!valid_array(X, x_type) || !valid_pitch(t, k, ldx) || !valid_checkpoint(q, ldq, scale, lds, k))
+    return ECASQ_ERR_ARG;
   return cuda_status(launch_checkpoint8(X, x_type, t, k, ldx, seed, seed_add, q, ldq, scale, lds,
                                         static_cast<cudaStream_t>(stream)));
 }
@@ -547,7 +554,8 @@ int ecasq_checkpoint8_restore(const int8_t* q, int64_t ldq, const uint8_t* scale
                               void* X, int x_type, int64_t ldx, void* stream) {
   if (!valid_type(x_type) || !valid_rows(t, k)) return ECASQ_ERR_ARG;
   if (t == 0) return ECASQ_OK;
-  if (!X || !valid_pitch(t, k, ldx) || !valid_checkpoint(q, ldq, scale, lds, k)) return ECASQ_ERR_ARG;
+  if (!valid_array(X, x_type) || !valid_pitch(t, k, ldx) || !valid_checkpoint(q, ldq, scale, lds, k))
+    return ECASQ_ERR_ARG;
   return cuda_status(
       launch_checkpoint8_restore(q, ldq, scale, lds, t, k, X, x_type, ldx, static_cast<cudaStream_t>(stream)));
 }
@@ -563,8 +571,9 @@ int ecasq_checkpoint8_wgrad(const void* dY, int dy_type, int64_t ldy, const int8
                             int64_t ldw, void* ws, size_t ws_bytes, void* stream) {
   if (!valid_type(dy_type) || !valid_type(dw_type) || !valid_rows(t, k) || o < 1 || o > kMaxCols8)
     return ECASQ_ERR_ARG;
-  if (!dW || !valid_pitch(o, k, ldw)) return ECASQ_ERR_ARG;
-  if (t > 0 && (!dY || !valid_pitch(t, o, ldy) || !valid_checkpoint(q, ldq, scale, lds, k))) return ECASQ_ERR_ARG;
+  if (!valid_array(dW, dw_type) || !valid_pitch(o, k, ldw)) return ECASQ_ERR_ARG;
+  if (t > 0 && (!valid_array(dY, dy_type) || !valid_pitch(t, o, ldy) || !valid_checkpoint(q, ldq, scale, lds, k)))
+    return ECASQ_ERR_ARG;
   const size_t need = checkpoint8_wgrad_workspace(dY, dy_type, ldy, t, o, k);
   if (need && (!ws || ws_bytes < need || (reinterpret_cast<uintptr_t>(ws) & 15) != 0)) return ECASQ_ERR_WORKSPACE;
   return cuda_status(launch_checkpoint8_wgrad(dY, dy_type, ldy, q, ldq, scale, lds, t, o, k, dW, dw_type, ldw, ws,

@@ -324,7 +324,7 @@ int ecasq_rans_decode(const uint16_t* words, const int32_t* seg_len, const int64
 /* ---- 8-bit operators: integer linear layer, activation checkpoints ----
  *
  * Matrices here have their own row pitch (ld*, in elements); the elements of a
- * row are adjacent. Element types: ECASQ_F32, ECASQ_BF16, ECASQ_F16. Row counts
+ * row are adjacent and lie on element boundaries. Element types: ECASQ_F32, ECASQ_BF16, ECASQ_F16. Row counts
  * may be 0 (nothing is launched, except that a weight gradient over no tokens
  * is written as zeros) and at most 2^31 - 1024, column counts at most 2^26. These calls serve any stream of the current device and
  * share nothing between calls, so calls may overlap and may be captured into

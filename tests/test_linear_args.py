@@ -85,6 +85,21 @@ def test_gradient_arguments(lib):
     assert size(P16, 1, 64, -1, 64, 100) == 0 and size(P16, 1, 64, 4, 0, 100) == 0 and size(P16, 9, 64, 4, 64, 100) == 0
 
 
+def test_arrays_off_their_elements(lib):
+    """Matrices of a type given at run time that start inside an element are refused."""
+    for ty, off in [(0, 2), (0, 1), (1, 1), (2, 1)]:
+        bad = C.c_void_p(P16.value + off)
+        assert lib.ecasq_int8_quantize(bad, ty, 4, 100, 100, P16, 112, P16, P16, NULL) == -1
+        assert lib.ecasq_int8_matmul(P16, 112, P16, P16, 112, P16, NULL, 4, 8, 100, bad, ty, 8, NULL) == -1
+        for x, y in [(bad, P16), (P16, bad)]:
+            assert lib.ecasq_int8_linear(x, ty, 100, P16, 112, P16, NULL, 40, 8, 100, y, 8, P16, 1 << 20, NULL) == -1
+        assert lib.ecasq_checkpoint8(bad, ty, 4, 100, 100, 7, NULL, P16, 128, P16, 16, NULL) == -1
+        assert lib.ecasq_checkpoint8_restore(P16, 128, P16, 16, 4, 100, bad, ty, 100, NULL) == -1
+        for dy, dw in [(bad, P16), (P16, bad)]:
+            assert lib.ecasq_checkpoint8_wgrad(dy, ty, 64, P16, 128, P16, 16, 4, 64, 100, dw, ty, 100, P16, 1 << 40,
+                                               NULL) == -1
+
+
 def test_gradient_workspace(lib):
     """Null, short and misaligned workspaces are refused: dY is copied into bf16 terms (float16, float32, rows off the
     16-byte boundary), or the sum over the tokens is split."""
