@@ -715,7 +715,8 @@ cudaError_t launch_checkpoint8_wgrad(const void* dY, int dy_type, int64_t ldy, c
 
 cudaError_t checkpoint8_stalled(bool* stalled) {
   int v = 0;
-  cudaError_t e = cudaMemcpyFromSymbol(&v, g_stalled_checkpoint8, sizeof(v));
+  cudaError_t e = cudaDeviceSynchronize();  // the copy alone does not wait for non-blocking streams
+  if (e == cudaSuccess) e = cudaMemcpyFromSymbol(&v, g_stalled_checkpoint8, sizeof(v));
   *stalled = v != 0;
   if (e == cudaSuccess && v) {
     v = 0;

@@ -749,7 +749,8 @@ cudaError_t launch_int8_linear(const void* X, int x_type, int64_t ldx, const int
 
 cudaError_t int8_stalled(bool* stalled) {
   int v = 0;
-  cudaError_t e = cudaMemcpyFromSymbol(&v, g_stalled_int8, sizeof(v));
+  cudaError_t e = cudaDeviceSynchronize();  // the copy alone does not wait for non-blocking streams
+  if (e == cudaSuccess) e = cudaMemcpyFromSymbol(&v, g_stalled_int8, sizeof(v));
   *stalled = v != 0;
   if (e == cudaSuccess && v) {
     v = 0;

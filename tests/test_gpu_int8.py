@@ -266,3 +266,16 @@ def test_few_tokens_around_48_kb():
     root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
     run = subprocess.run([sys.executable, "-c", LONG_FEW], cwd=root, capture_output=True, text=True, timeout=300)
     assert run.returncode == 0, run.stderr[-2000:]
+
+
+def test_check_stalled_waits_for_every_stream(E):
+    """The check returns after what runs on a stream that does not wait for the default one."""
+    E.check_stalled()  # first: the library's symbols are loaded, which may wait by itself
+    A, sa, B, sb, bias = _operands(40, 4096, 4096, 4096)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        for _ in range(200):  # tens of milliseconds
+            E.int8_matmul(A, sa, B, sb, bias)
+    E.check_stalled()
+    assert side.query()
