@@ -511,8 +511,7 @@ __global__ void __launch_bounds__(256)
 // dW = the sum of `split` partial matrices [o][k], in their order.
 template <int kOut>
 __global__ void __launch_bounds__(256)
-    k_join(const float* __restrict__ part, int split, int64_t o, int64_t k, typename Elem<kOut>::T* __restrict__ dW,
-           int64_t ldw) {
+    k_join(const float* part, int split, int64_t o, int64_t k, typename Elem<kOut>::T* dW, int64_t ldw) {
   after_previous();
   const int64_t c = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
   if (c >= k) return;
@@ -520,7 +519,7 @@ __global__ void __launch_bounds__(256)
     float sum = 0.0f;
     const float* from = part + r * k + c;
 #pragma unroll 16
-    for (int i = 0; i < split; ++i) sum += __ldg(from + i * (o * k));
+    for (int i = 0; i < split; ++i) sum += from[i * (o * k)];
     dW[r * ldw + c] = Elem<kOut>::put(sum);
   }
 }

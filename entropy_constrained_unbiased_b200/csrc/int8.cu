@@ -296,7 +296,7 @@ __global__ void __launch_bounds__(192, 2)
 #pragma unroll
         for (int j = 0; j < kCols; ++j)
           if (live && j0 + j < tokens)
-            put_output<kType>(p, token0 + j0 + j, channel, static_cast<int>(v[j]), __ldg(p.sa + token0 + j0 + j), s, bias);
+            put_output<kType>(p, token0 + j0 + j, channel, static_cast<int>(v[j]), p.sa[token0 + j0 + j], s, bias);
       } else {
 #pragma unroll
         for (int j = 0; j < kCols; ++j)
@@ -328,7 +328,7 @@ __global__ void __launch_bounds__(192, 2)
 #pragma unroll
           for (int u = 0; u < kAtOnce; ++u) {
             const int j = j0 + u * split;
-            if (j < tokens) put_output<kType>(p, token0 + j, channel, sum[u], __ldg(p.sa + token0 + j), s, bias);
+            if (j < tokens) put_output<kType>(p, token0 + j, channel, sum[u], p.sa[token0 + j], s, bias);
           }
         }
       }
@@ -531,7 +531,7 @@ constexpr int kFewThreads = 256;
 // kIn: the tokens' type, or -1 for rows that are quantised already (A, sa).
 template <int kIn, int kType, int kM>
 __global__ void __launch_bounds__(kFewThreads)
-    k_int8_few(const void* __restrict__ X, int64_t ldx, bool wide, const int8_t* __restrict__ B, int64_t ldb,
+    k_int8_few(const void* X, int64_t ldx, bool wide, const int8_t* __restrict__ B, int64_t ldb,
                const Product p, int64_t k) {
   extern __shared__ int4 tokens[];  // [m][kp / 16]
   __shared__ uint32_t part[kFewThreads / 32];
@@ -586,7 +586,7 @@ __global__ void __launch_bounds__(kFewThreads)
 #pragma unroll 8
     for (int i = threadIdx.x; i < m * kp; i += kFewThreads) {
       const int j = i / kp, c = i - j * kp;
-      if (c < whole) tokens[i] = __ldg(reinterpret_cast<const int4*>(x + j * ldx) + c);
+      if (c < whole) tokens[i] = reinterpret_cast<const int4*>(x + j * ldx)[c];
     }
     for (int i = threadIdx.x; i < m * tail; i += kFewThreads) {
       const int j = i / tail, c = whole * 16 + i - j * tail;

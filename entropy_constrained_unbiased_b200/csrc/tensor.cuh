@@ -33,7 +33,8 @@ inline int sm_count() {
 // Launches a kernel that may begin before the previous kernel of the stream, this
 // library's own and launched just before, has ended (`early`): its set-up and its
 // reads of what that kernel does not write overlap it; what it does write is read
-// after after_previous(). That kernel calls next_may_begin().
+// after after_previous(), by plain loads (the read-only path is for what nobody writes
+// while the kernel lives). That kernel calls next_may_begin().
 template <typename... Params, typename... Args>
 cudaError_t launch_kernel(void (*kernel)(Params...), dim3 grid, unsigned threads, size_t smem, cudaStream_t st,
                           unsigned cluster, bool early, Args&&... args) {

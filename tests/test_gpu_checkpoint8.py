@@ -400,6 +400,30 @@ def test_linear_of_transposed_and_expanded_inputs(E):
         assert torch.equal(int8_linear(x, wq, ws), int8_linear(x.contiguous(), wq, ws))
 
 
+def test_chained_launches_read_what_the_kernel_before_wrote(E):
+    """Calls of two and three kernels back to back on one stream, whose workspaces the allocator gives to each in turn:
+    each result is that of its own inputs (token scales, quantised tokens, bf16 terms, partial sums)."""
+    wq, ws, _ = E.int8_quantize(_x(1, 300, 4096, torch.float32))
+    xs = [[_x(100 * m + i, m, 4096, torch.bfloat16, 2.0**i) for i in range(4)] for m in (2, 9, 100, 300)]
+    q, b = E.checkpoint8(_x(2, 6000, 96, torch.float32), 3)
+    dys = [_x(50 + i, 6000, 64, dtype, 2.0**i) for dtype in TYPES for i in range(3)]
+    def separately(x):
+        a, s, _ = E.int8_quantize(x)
+        torch.cuda.synchronize()
+        return E.int8_matmul(a, s, wq, ws, None, x.dtype)
+    want = [[separately(x) for x in group] for group in xs]
+    for _ in range(20):
+        for group, w in zip(xs, want):
+            got = [E.int8_linear(x, wq, ws) for x in group]
+            assert all(torch.equal(g, r) for g, r in zip(got, w))
+        grads = [E.checkpoint8_wgrad(dY, q, b) for dY in dys]
+        torch.cuda.synchronize()
+        for dY, dW in zip(dys, grads):
+            assert torch.equal(dW, E.checkpoint8_wgrad(dY, q, b))
+    for dY, dW in zip(dys, grads):
+        _check_gradient(E, dY, q, b)
+
+
 def test_training_step_in_a_graph(E):
     """Forward and backward captured once and replayed with new inputs and a new seed word equal the eager step."""
     from entropy_constrained_unbiased_b200.linear import checkpoint_linear
