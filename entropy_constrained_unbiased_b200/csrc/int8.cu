@@ -276,7 +276,7 @@ __global__ void __launch_bounds__(192, 2)
     if (elected) mma_commit<1>(done);
   } else {
     after_previous();
-    ok = mbar_wait_bounded(done, 0, kWaitLimit);
+    ok = __all_sync(0xffffffffu, mbar_wait_bounded(done, 0, kWaitLimit));
     tcgen05_after_sync();
     const int64_t channel = channel0 + warp * 32 + lane;
     const int tokens = static_cast<int>(min(static_cast<int64_t>(kTok), p.m - token0));
@@ -473,9 +473,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
       const bool live = channel < p.n;
       const float s = live ? p.sb[channel] : 0.0f;
       const float bias = live && p.bias ? p.bias[channel] : 0.0f;
-      asm volatile("bar.sync 1, 256;" ::: "memory");
-      ok = __all_sync(0xffffffffu, mbar_wait_bounded(done + 8 * buf, (n >> 1) & 1, kWaitLimit));
+      // the eight warps leave together: none waits here for one whose last wait ran out
+      ok = barrier_and(1, 256, ok);
       if (!ok) break;
+      ok = __all_sync(0xffffffffu, mbar_wait_bounded(done + 8 * buf, (n >> 1) & 1, kWaitLimit));
+      if (!ok) continue;
       tcgen05_after_sync();
       const int half = (warp >> 2) * 128, end = min(tokens, half + 128);  // this warp's tokens
       for (int j0 = half; j0 < end; j0 += 32) {

@@ -129,6 +129,18 @@ __device__ __forceinline__ void mbar_arrive_cluster(uint32_t mbar) {
   asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(mbar) : "memory");
 }
 
+// Named barrier of `threads` threads: whether all of them brought true.
+__device__ __forceinline__ bool barrier_and(int id, int threads, bool mine) {
+  uint32_t all;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 q, %3, 0;\n\tbarrier.cta.red.and.aligned.pred p, %1, %2, q;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(all)
+      : "r"(id), "r"(threads), "r"(static_cast<uint32_t>(mine))
+      : "memory");
+  return all != 0;
+}
+
 // A place in a ring of kStages stages, walked in order: the stage, the parity of the
 // current round, and whether it is the first one. (Divisions of a running count cost
 // a single-threaded role hundreds of clocks per stage.)

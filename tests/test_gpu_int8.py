@@ -127,6 +127,15 @@ def test_product(E, m, n, k):
         _check_product(E, A, sa, B, sb, bias if i != 1 else None, dtype)
 
 
+@pytest.mark.parametrize("m,n,k", [(1300, 4400, 640), (4500, 4200, 200), (20000, 300, 100), (300, 20000, 96)])
+def test_product_of_more_tiles_than_pairs(E, m, n, k):
+    """Pairs of CTAs that take several tiles each (either accumulator and its token scales in turn), channels beyond the
+    first block of 4096."""
+    A, sa, B, sb, bias = _operands(m + n + k, m, n, k)
+    for i, dtype in enumerate(TYPES):
+        _check_product(E, A, sa, B, sb, bias if i != 1 else None, dtype)
+
+
 @pytest.mark.parametrize("m", [1, 20, 300])
 def test_product_largest_sums(E, m):
     """Every product 127^2 at the longest sum: just below 2^31."""
