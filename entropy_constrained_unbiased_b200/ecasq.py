@@ -526,11 +526,8 @@ def _vector(t, name, n, index):
 
 
 def _rows8(like, n, k, to, dtype):
-    """Uninitialised 8-bit values on like's device in rows of a whole number of `to` bytes: all of them, and the
-    [n, k] part."""
-    kp = (k + to - 1) // to * to
-    t = like.new_empty((n, kp), dtype=dtype)
-    return t, (t if kp == k else t[:, :k])
+    """Uninitialised 8-bit values [n, k] on like's device, in whole rows of a multiple of `to` bytes."""
+    return like.new_empty((n, (k + to - 1) // to * to), dtype=dtype)
 
 
 def _elsewhere(index):
@@ -549,14 +546,14 @@ def int8_quantize(X: torch.Tensor):
         with torch.cuda.device(index):
             return int8_quantize(X)
     n, k, ld = _matrix(X, "X", _TYPES)
-    rows, q = _rows8(X, n, k, 32, torch.int8)
+    rows = _rows8(X, n, k, 32, torch.int8)
     scale = X.new_empty(n, dtype=torch.float32)
     st = X.new_empty(n, dtype=torch.int32)
     rc = _lib.ecasq_int8_quantize(X.data_ptr(), _TYPES[X.dtype], n, k, ld, rows.data_ptr(), rows.shape[1],
                                   scale.data_ptr(), st.data_ptr(), _stream_of(index))
     if rc:
         _check(rc, "ecasq_int8_quantize")
-    return q, scale, st
+    return rows if rows.shape[1] == k else rows[:, :k], scale, st
 
 
 def _weights(B, sb, bias, k, index):
@@ -620,10 +617,22 @@ def checkpoint8(X: torch.Tensor, seed):
     q int8 [t, k] and the scale bytes uint8 [t, ceil(k / 32)] of its blocks of 32
     entries. `seed` is an integer, or a CUDA int64 tensor of one entry read when
     the call runs (a graph's replays then draw new bits when it changes)."""
+    q, scale = _checkpoint8(X, seed)
+    return _part8(q, scale, X.shape[1])
+
+
+def _part8(q, scale, k):
+    """The entries and blocks of k columns in the whole rows of a checkpoint."""
+    blocks = (k + 31) // 32
+    return q if q.shape[1] == k else q[:, :k], scale if scale.shape[1] == blocks else scale[:, :blocks]
+
+
+def _checkpoint8(X, seed):
+    """checkpoint8 as the whole rows that it lies in, which stay so when they are copied."""
     index = X.get_device()
     if _elsewhere(index):
         with torch.cuda.device(index):
-            return checkpoint8(X, seed)
+            return _checkpoint8(X, seed)
     t, k, ld = _matrix(X, "X", _TYPES)
     word = None
     if isinstance(seed, torch.Tensor):
@@ -632,11 +641,10 @@ def checkpoint8(X: torch.Tensor, seed):
         seed, word = 0, seed.data_ptr()
     elif not isinstance(seed, int):
         raise EcasqError(f"seed must be an integer or a CUDA int64 tensor of one entry, not {type(seed).__name__}")
-    q_rows, q = _rows8(X, t, k, 32, torch.int8)
-    s_rows, s = _rows8(X, t, (k + 31) // 32, 16, torch.uint8)
+    q = _rows8(X, t, k, 32, torch.int8)
+    s = _rows8(X, t, (k + 31) // 32, 16, torch.uint8)
     rc = _lib.ecasq_checkpoint8(X.data_ptr(), _TYPES[X.dtype], t, k, ld, seed & 0xFFFFFFFFFFFFFFFF, word,
-                                q_rows.data_ptr(), q_rows.shape[1], s_rows.data_ptr(), s_rows.shape[1],
-                                _stream_of(index))
+                                q.data_ptr(), q.shape[1], s.data_ptr(), s.shape[1], _stream_of(index))
     if rc:
         _check(rc, "ecasq_checkpoint8")
     return q, s

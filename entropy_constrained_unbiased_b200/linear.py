@@ -45,10 +45,12 @@ class _CheckpointLinear(torch.autograd.Function):
     @torch.amp.custom_fwd(device_type="cuda")
     def forward(ctx, x, weight, bias, seed):
         if ctx.needs_input_grad[1]:
-            q, scale = E.checkpoint8(_rows(x), seed)
+            # whole rows: a hook may copy what is saved, and a part's copy would lose their pitch
+            q, scale = E._checkpoint8(_rows(x), seed)
         else:
             q = scale = None
         ctx.save_for_backward(q, scale, weight if ctx.needs_input_grad[0] else None)
+        ctx.columns = x.shape[-1]
         ctx.dtypes = x.dtype, weight.dtype, None if bias is None else bias.dtype
         return F.linear(x, weight, bias)
 
@@ -63,6 +65,7 @@ class _CheckpointLinear(torch.autograd.Function):
             dx = torch.matmul(dy, weight).to(x_type)
         rows = _rows(dy)
         if ctx.needs_input_grad[1]:
+            q, scale = E._part8(q, scale, ctx.columns)
             dw = E.checkpoint8_wgrad(rows, q, scale, w_type)
         if ctx.needs_input_grad[2]:
             db = rows.sum(0, dtype=torch.float32).to(b_type)

@@ -323,6 +323,24 @@ def test_linear_weight_gradient_by_differences(E):
     assert (slope - (w.grad.double() * direction).sum()).abs() <= 3 * 60 * 2.0**-23 * size
 
 
+@pytest.mark.parametrize("k", [512, 768, 777])
+def test_linear_under_saved_tensor_hooks(E, k):
+    """What the layer keeps may be copied elsewhere and back (offload), whatever the width."""
+    from entropy_constrained_unbiased_b200.linear import checkpoint_linear
+    x, w = _x(1, 20, k, torch.bfloat16), _x(2, 10, k, torch.bfloat16).requires_grad_()
+    dy = _x(3, 20, 10, torch.bfloat16)
+    (want,) = torch.autograd.grad(checkpoint_linear(x, w, seed=3), w, dy)
+    with torch.autograd.graph.save_on_cpu():
+        y = checkpoint_linear(x, w, seed=3)
+    assert torch.equal(torch.autograd.grad(y, w, dy)[0], want)
+    with torch.autograd.graph.saved_tensors_hooks(lambda t: t.clone(memory_format=torch.contiguous_format), lambda t: t):
+        y = checkpoint_linear(x[:1], w, seed=3)
+        z = checkpoint_linear(x[:0], w, seed=3)
+    (got,) = torch.autograd.grad(y, w, dy[:1])
+    assert torch.equal(got, torch.autograd.grad(checkpoint_linear(x[:1], w, seed=3), w, dy[:1])[0])
+    assert not torch.autograd.grad(z, w, dy[:0])[0].any()
+
+
 def test_linear_mean_gradient(E):
     """The mean over seeds is the gradient of the unrounded layer, within 5 standard errors."""
     from entropy_constrained_unbiased_b200.linear import checkpoint_linear
