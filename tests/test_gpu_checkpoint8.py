@@ -153,6 +153,14 @@ def test_weight_gradient(E, t, o, k):
         _check_gradient(E, dY, q, b, torch.float32)
 
 
+@pytest.mark.parametrize("t,o,k", [(130, 2500, 2400), (300, 40, 20000), (70, 20000, 300), (1500, 2600, 2100)])
+def test_weight_gradient_of_more_tiles_than_pairs(E, t, o, k):
+    """Pairs of CTAs that take several tiles each, of one accumulator or several."""
+    q, b = E.checkpoint8(_x(t + o, t, k, torch.float32), 3)
+    for dtype in TYPES:
+        _check_gradient(E, _x(t + k, t, o, dtype, 0.01), q, b)
+
+
 def test_weight_gradient_float32_sums(E):
     """float32 results over a long sum stay within 2e-6 of the norm: the sums are not kept in fewer bits."""
     q, b = E.checkpoint8(_x(1, 8192, 256, torch.float32), 3)
