@@ -84,4 +84,6 @@ def checkpoint_linear(x: torch.Tensor, weight: torch.Tensor, bias=None, *, seed)
         raise E.EcasqError("checkpoint_linear needs x and weight on one CUDA device; there is no CPU path")
     if weight.dim() != 2 or x.dim() < 1 or x.shape[-1] != weight.shape[1]:
         raise E.EcasqError(f"x [..., k] and weight [n, k] do not match: {list(x.shape)}, {list(weight.shape)}")
+    if not torch.is_grad_enabled():
+        return F.linear(x, weight, bias)  # nothing is kept
     return _CheckpointLinear.apply(x, weight, bias, seed)

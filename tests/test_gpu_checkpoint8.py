@@ -378,6 +378,21 @@ def test_linear_of_a_sum_and_without_weight_gradient(E):
         assert not checkpoint_linear(x, w, seed=1).requires_grad
 
 
+def test_linear_without_gradients_stores_nothing(E):
+    """Evaluation with trainable weights is F.linear: no kernel of the library runs."""
+    from entropy_constrained_unbiased_b200.linear import checkpoint_linear
+    import torch.nn.functional as F
+    x, w = _x(1, 20, 64, torch.bfloat16), _x(2, 10, 64, torch.bfloat16).requires_grad_()
+    L = E.load()
+    before = L.ecasq_launch_count(0)
+    for mode in (torch.no_grad, torch.inference_mode):
+        with mode():
+            assert torch.equal(checkpoint_linear(x, w, seed=1), F.linear(x, w))
+    assert L.ecasq_launch_count(0) == before
+    checkpoint_linear(x, w, seed=1)
+    assert L.ecasq_launch_count(0) == before + 1
+
+
 def test_linear_under_autocast(E):
     from entropy_constrained_unbiased_b200.linear import checkpoint_linear
     x, w = _x(1, 20, 64, torch.float32).requires_grad_(), _x(2, 10, 64, torch.float32).requires_grad_()
