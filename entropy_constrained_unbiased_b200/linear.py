@@ -30,9 +30,10 @@ def int8_linear(x: torch.Tensor, weight: torch.Tensor, weight_scale: torch.Tenso
     """x [..., k] (float32, bfloat16 or float16) times 8-bit weights: quantises each
     token and multiplies, Y [..., n] in x's type. weight int8 [n, k] and
     weight_scale float32 [n] are ecasq.int8_quantize's of the layer's weight
-    matrix; bias float32 [n]. For serving: it has no gradient, and refuses an x
-    that asks for one."""
-    if x.requires_grad and torch.is_grad_enabled():
+    matrix; bias float32 [n]. For serving: it has no gradient, and refuses an x,
+    a scale or a bias that asks for one."""
+    if torch.is_grad_enabled() and (x.requires_grad or weight_scale.requires_grad
+                                    or (bias is not None and bias.requires_grad)):
         raise E.EcasqError("int8_linear has no gradient; use checkpoint_linear for training, or torch.no_grad()")
     if x.dim() == 0:
         raise E.EcasqError("x must have at least one dimension")

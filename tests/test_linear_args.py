@@ -123,6 +123,19 @@ def test_no_cpu_path():
             call()
 
 
+def test_int8_linear_refuses_gradients():
+    """No operand's gradient is silently lost (looked at before the device)."""
+    from entropy_constrained_unbiased_b200 import ecasq as E
+    from entropy_constrained_unbiased_b200.linear import int8_linear
+    x, w, s = torch.zeros((2, 32)), torch.zeros((2, 32), dtype=torch.int8), torch.zeros(2)
+    grad = lambda t: t.clone().requires_grad_()
+    for args in ((grad(x), w, s), (x, w, grad(s)), (x, w, s, grad(s)), (x, w, s.clone(), grad(s))):
+        with pytest.raises(E.EcasqError, match="no gradient"):
+            int8_linear(*args)
+        with torch.no_grad(), pytest.raises(E.EcasqError, match="CUDA"):
+            int8_linear(*args)
+
+
 @pytest.mark.gpu
 def test_binding_refusals():
     """Types, shapes, layouts and devices that the binding refuses before the library is called."""
