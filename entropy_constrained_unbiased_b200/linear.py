@@ -26,18 +26,32 @@ def _rows(x):
     return rows.contiguous() if (k > 1 and one != 1) or (n > 1 and ld < k) else rows
 
 
+def _whole_rows(weight):
+    """8-bit weights in rows of whole 16 bytes: as they are, or a copy of dense rows of another length."""
+    if weight.dim() != 2 or weight.dtype != torch.int8:
+        return weight
+    n, k = weight.shape
+    if (k if n == 1 else weight.stride(0)) % 16 == 0:  # the pitch of a single row says nothing
+        return weight
+    return F.pad(weight, (0, -k % 16))[:, :k]
+
+
 def int8_linear(x: torch.Tensor, weight: torch.Tensor, weight_scale: torch.Tensor, bias=None) -> torch.Tensor:
     """x [..., k] (float32, bfloat16 or float16) times 8-bit weights: quantises each
     token and multiplies, Y [..., n] in x's type. weight int8 [n, k] and
     weight_scale float32 [n] are ecasq.int8_quantize's of the layer's weight
     matrix; bias float32 [n]. For serving: it has no gradient, and refuses an x,
-    a scale or a bias that asks for one."""
+    a scale or a bias that asks for one.
+
+    int8_quantize lays rows out in whole 32 bytes. Weights that lost this (a dense
+    copy, a loaded state, of a k that is no multiple of 16) are copied in every
+    call; F.pad(weight, (0, -k % 16))[:, :k], kept, saves that."""
     if torch.is_grad_enabled() and (x.requires_grad or weight_scale.requires_grad
                                     or (bias is not None and bias.requires_grad)):
         raise E.EcasqError("int8_linear has no gradient; use checkpoint_linear for training, or torch.no_grad()")
     if x.dim() == 0:
         raise E.EcasqError("x must have at least one dimension")
-    y = E.int8_linear(_rows(x), weight, weight_scale, bias)
+    y = E.int8_linear(_rows(x), _whole_rows(weight), weight_scale, bias)
     return y if x.dim() == 2 else y.reshape(*x.shape[:-1], y.shape[1])
 
 

@@ -198,6 +198,20 @@ def test_linear_equals_its_two_steps(E, m, n, k, dtype):
     assert torch.equal(E.int8_linear(off[:, 3:], wq, ws).nan_to_num(7.0), E.int8_linear(x, wq, ws).nan_to_num(7.0))
 
 
+@pytest.mark.parametrize("n,k", [(1, 777), (40, 777), (40, 33), (40, 1), (40, 768)])
+def test_linear_with_dense_copies_of_the_weights(E, n, k):
+    """Weights that lost their rows' padding on the way (a clone, a round trip through the host, a loaded state)."""
+    from entropy_constrained_unbiased_b200.linear import int8_linear
+    wq, ws, _ = E.int8_quantize(_x(9, n, k, torch.float32))
+    x = _x(10, 5, k, torch.bfloat16)
+    want = int8_linear(x, wq, ws)
+    layer = torch.nn.Module()
+    layer.register_buffer("weight", torch.zeros((n, k), dtype=torch.int8, device="cuda"))
+    layer.load_state_dict({"weight": wq})
+    for w in (wq.clone(memory_format=torch.contiguous_format), wq.cpu().cuda(), layer.weight):
+        assert torch.equal(int8_linear(x, w, ws), want)
+
+
 def test_linear_refuses_a_gradient(E):
     from entropy_constrained_unbiased_b200.linear import int8_linear
     wq, ws, _ = E.int8_quantize(_x(9, 40, 64, torch.float32))
