@@ -174,12 +174,17 @@ struct Product {
   bool early;  // launched behind the quantiser of the tokens
 };
 
+// The exact sum behind a 32-bit accumulator that wraps around. The least sum of 131072
+// products, of -128 by 127, is above -2^31, so that value stands for the one sum that
+// wraps: 2^31, all products being -128 by -128.
+__device__ __forceinline__ float sum_value(int acc) { return acc == INT32_MIN ? 0x1p31f : static_cast<float>(acc); }
+
 // One output: the exact integer sum, scaled.
 template <int kType>
 __device__ __forceinline__ void put_output(const Product& p, int64_t token, int64_t channel, int acc, float a, float s,
                                            float bias) {
   static_cast<typename Elem<kType>::T*>(p.Y)[token * p.ldy + channel] =
-      Elem<kType>::put(fmaf(static_cast<float>(acc) * a, s, bias));
+      Elem<kType>::put(fmaf(sum_value(acc) * a, s, bias));
 }
 
 // -- up to 128 tokens: a tile of 128 channels by kTok tokens per cluster, k split over the
@@ -318,17 +323,17 @@ __global__ void __launch_bounds__(192, 2)
         const float s = p.sb[channel], bias = p.bias ? p.bias[channel] : 0.0f;
         constexpr int kAtOnce = 8;  // tokens of this CTA's share whose partial sums are in flight
         for (int j0 = part; j0 < tokens; j0 += split * kAtOnce) {
-          int sum[kAtOnce] = {};
+          uint32_t sum[kAtOnce] = {};
           for (int r = 0; r < split; ++r) {
             const uint32_t from = map_shared(tiles + 4 * (warp * 32 + lane), r);
 #pragma unroll
             for (int u = 0; u < kAtOnce; ++u)
-              if (j0 + u * split < tokens) sum[u] += ld_shared_cluster(from + 512 * (j0 + u * split));
+              if (j0 + u * split < tokens) sum[u] += static_cast<uint32_t>(ld_shared_cluster(from + 512 * (j0 + u * split)));
           }
 #pragma unroll
           for (int u = 0; u < kAtOnce; ++u) {
             const int j = j0 + u * split;
-            if (j < tokens) put_output<kType>(p, token0 + j, channel, sum[u], p.sa[token0 + j], s, bias);
+            if (j < tokens) put_output<kType>(p, token0 + j, channel, static_cast<int>(sum[u]), p.sa[token0 + j], s, bias);
           }
         }
       }

@@ -347,7 +347,7 @@ int ecasq_int8_quantize(const void* X, int x_type, int64_t n, int64_t k, int64_t
 /* Product of 8-bit integers with a scale per token and per output channel:
  *   Y[i][j] = (sum_l A[i][l] B[j][l]) * sa[i] * sb[j] + bias[j],
  * A [m][k] (tokens), B [n][k] (output channels), bias [n] float32 or NULL. The
- * integer sum is exact (32 bits: k <= 131072), the scales are applied in
+ * integer sum is exact for any bytes (k <= 131072), the scales are applied in
  * float32 and the result is rounded once to y_type. lda, ldb are multiples of
  * 16 and A, B 16-byte aligned. */
 int ecasq_int8_matmul(const int8_t* A, int64_t lda, const float* sa, const int8_t* B, int64_t ldb, const float* sb,

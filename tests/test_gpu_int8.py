@@ -143,6 +143,19 @@ def test_product_largest_sums(E, m):
     _check_product(E, A, sa, B, sb, None, torch.float32)
 
 
+@pytest.mark.parametrize("m", [1, 2, 20, 300])
+def test_product_of_the_least_integers(E, m):
+    """Every product (-128)^2 at the longest sum is 2^31; its neighbours, and the least sum, lie inside 32 bits."""
+    A = torch.full((m, 131072), -128, dtype=torch.int8, device="cuda")
+    B = torch.full((140, 131072), -128, dtype=torch.int8, device="cuda")
+    B[1, 5], B[2, 7], B[3] = -127, 127, 127
+    ones = torch.ones(300, device="cuda")
+    Y = E.int8_matmul(A, ones[:m], B, ones[:140], None, torch.float32)
+    want = torch.full((140,), 2**31, dtype=torch.float64, device="cuda")
+    want[1], want[2], want[3] = 2**31 - 128, 2**31 - 128 * 255, -128 * 127 * 131072
+    assert torch.equal(Y, want.float().expand(m, 140))
+
+
 @pytest.mark.parametrize("m", [1, 5, 70, 300])
 def test_product_rows_inside_wider_matrices(E, m):
     A, sa, B, sb, bias = _operands(6, 2 * m, 400, 512)
