@@ -156,6 +156,36 @@ def test_product_of_the_least_integers(E, m):
     assert torch.equal(Y, want.float().expand(m, 140))
 
 
+@pytest.mark.parametrize("m", [2, 20, 300])
+@pytest.mark.parametrize("ea,eb", [(118, -60), (96, 0), (-133, 100), (-140, 110), (-94, 0), (60, 40), (-100, -20), (100, 100)])
+def test_product_with_extreme_scales(E, m, ea, eb):
+    """Token scales near either end of float32: what the two scales give together is what counts."""
+    A, sa, B, sb, bias = _operands(3, m, 40, 4096)
+    sa, sb = (sa.double() * 2.0**ea).float(), (sb.double() * 2.0**eb).float()
+    sa[0], A[0, 7] = 0, 5
+    if ea + eb == 200:
+        Y = E.int8_matmul(A, sa, B, sb, bias, torch.float32)
+        assert torch.equal(Y[0], bias) and torch.isinf(Y[1:]).all()
+        return
+    _check_product(E, A, sa, B, sb, None, torch.float32)
+    _check_product(E, A, sa, B, sb, bias, torch.float32)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("m", [1, 12, 200])
+def test_linear_of_huge_and_tiny_tokens(E, m, dtype):
+    """Tokens near the type's largest values, and near its smallest, through weights that bring them back."""
+    w = torch.randn((30, 512), generator=torch.Generator().manual_seed(1)).cuda()
+    x = torch.randn((m, 512), generator=torch.Generator().manual_seed(2)).clamp(-3, 3).cuda()
+    for ex, ew in ((126, -30), (-126, 90)):
+        wq, ws, _ = E.int8_quantize(w * 2.0**ew)
+        t = (x.double() * 2.0**ex / 4).to(dtype)
+        q, s, _ = E.int8_quantize(t)
+        y = E.int8_linear(t, wq, ws)
+        assert torch.equal(y, E.int8_matmul(q, s, wq, ws, None, dtype)) and torch.isfinite(y).all()
+        _check_product(E, q, s, wq, ws, None, dtype)
+
+
 @pytest.mark.parametrize("m", [1, 5, 70, 300])
 def test_product_rows_inside_wider_matrices(E, m):
     A, sa, B, sb, bias = _operands(6, 2 * m, 400, 512)
