@@ -481,7 +481,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGradThreads, 1)
 
 // dY [t][o] as bf16 terms [kTerms][t][ld], whose sum is dY exactly: each term is the rest
 // so far cut (not rounded: no overflow) to its upper 8 bits; the largest term is the
-// last one. What is not finite is the last term, with zeros before it.
+// last one. (Of a float32 entry below 2^-110 the third term cuts what is under 2^-133,
+// bfloat16's smallest value.) What is not finite is the last term, with zeros before it.
 template <int kIn, int kTerms>
 __global__ void __launch_bounds__(256)
     k_terms(const typename Elem<kIn>::T* __restrict__ dY, int64_t ldy, bool wide, int64_t t, int64_t o,

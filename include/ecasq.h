@@ -393,8 +393,9 @@ int ecasq_checkpoint8_restore(const int8_t* q, int64_t ldq, const uint8_t* scale
 /* Weight gradient of a linear layer Y = X W^T from the checkpoint of X:
  *   dW[i][j] = sum_r dY[r][i] s[r][j / 32] q[r][j],  dY [t][o], dW [o][k].
  * Products are exact (a float16 or float32 dY is taken apart into two or three
- * bfloat16 terms whose sum it is), sums are float32, the result is rounded once
- * to dw_type. Long sums over few output entries are split over the tokens and
+ * bfloat16 terms whose sum it is; of a float32 entry below 2^-110, the bits
+ * under 2^-133 are cut), sums are float32, the result is rounded once to
+ * dw_type. Long sums over few output entries are split over the tokens and
  * joined in a fixed order, so results repeat. Workspace, 16-byte aligned:
  * ecasq_checkpoint8_wgrad_workspace_size for the same dY (its address is not
  * read through, only its alignment counts), sizes and pitch on the current

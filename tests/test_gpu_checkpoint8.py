@@ -224,6 +224,24 @@ def test_weight_gradient_huge_and_tiny_gradients(E, dtype):
     assert dW[1, 3] == top and dW[2, 5] == -low and dW[4, 7] == dY[2, 4] and int((dW != 0).sum()) == 3
 
 
+@pytest.mark.parametrize("dtype", TYPES)
+def test_weight_gradient_of_small_entries(E, dtype):
+    """Entries down to the type's smallest, brought back by a large X: exact products, except for the bits of float32
+    entries that lie under 2^-133. One product per sum, so that nothing else is rounded but the result. (The largest float16
+    entries are infinities, and so are their products.)"""
+    q, b = E.checkpoint8(torch.full((1, 32), 2.0**100, device="cuda"), 1)
+    low = torch.tensor([SMALLEST[dtype]], dtype=torch.float64).log2().int().item()
+    m = 1 + torch.rand(64, generator=torch.Generator().manual_seed(1), dtype=torch.float64)
+    dY = torch.cat([m * 2.0**e for e in range(low, low + 60)]).to(dtype).cuda()[None]
+    dW = E.checkpoint8_wgrad(dY, q, b, torch.float32)
+    want = dY[0].double() * 2.0**100
+    cut = 2.0**-133 if dtype == torch.float32 else 0.0
+    off = torch.where(want.isinf()[:, None] & (dW == want[:, None]), 0.0, (dW.double() - want[:, None]).abs())
+    assert torch.all(off <= cut * 2.0**100)
+    exact = dY[0].abs().double() >= (2.0**-110 if dtype == torch.float32 else 0.0)
+    assert int(exact.sum()) >= 64 * 20 and torch.equal(dW[exact].double(), want[exact, None].expand(-1, 32))
+
+
 def test_weight_gradient_not_finite(E):
     """NaN and infinities of dY reach their row of dW alone, a marked block of X its 32 columns alone."""
     X = _x(1, 150, 200, torch.float32)
