@@ -126,7 +126,13 @@ __global__ void __launch_bounds__(256)
   const bool live = r < t && c * 8 < k;
   float v[8] = {};
   if (live) {
-    const uint2 w = __ldg(reinterpret_cast<const uint2*>(Q + r * ldq + c * 8));
+    const int8_t* from = Q + r * ldq + c * 8;
+    uint2 w = make_uint2(0, 0);
+    if (c * 8 + 8 <= k) {
+      w = __ldg(reinterpret_cast<const uint2*>(from));
+    } else {  // the memory of the last row may end with its entries
+      for (int e = 0; c * 8 + e < k; ++e) (e < 4 ? w.x : w.y) |= static_cast<uint32_t>(static_cast<uint8_t>(from[e])) << (8 * (e & 3));
+    }
     const float s = scale_value(S[r * lds + (c >> 2)]);
 #pragma unroll
     for (int e = 0; e < 8; ++e) {

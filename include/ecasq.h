@@ -379,7 +379,7 @@ int ecasq_int8_linear(const void* X, int x_type, int64_t ldx, const int8_t* B, i
  * A power of two makes q s exact in bfloat16, so the products of
  * ecasq_checkpoint8_wgrad add no rounding of their own to the unbiased values.
  * q [t][ldq]: ldq a multiple of 32, at least k; a row's last block is written
- * whole, with zeros beyond k. scale [t][lds]: lds a multiple of 16, at least
+ * whole, with zeros beyond k (which no call reads). scale [t][lds]: lds a multiple of 16, at least
  * ceil(k / 32); bytes beyond the blocks are not written. q and scale are
  * 16-byte aligned. */
 int ecasq_checkpoint8(const void* X, int x_type, int64_t t, int64_t k, int64_t ldx, uint64_t seed,

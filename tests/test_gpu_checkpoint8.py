@@ -101,6 +101,23 @@ def test_strides_and_neighbours(E):
     np.testing.assert_array_equal(q[:, :21].cpu().numpy(), plain8.checkpoint(_f64(X), 9)[0])
 
 
+def test_checkpoint_in_memory_that_ends_with_its_entries(E):
+    """The last row's padding is neither read nor needed, by the restore or the gradient: other bytes there change
+    nothing, and memory without them is taken."""
+    t, k, ldq, lds = 7, 77, 96, 16
+    q, b = E.checkpoint8(_x(1, t, k, torch.float32), 3)
+    dY = _x(2, t, 40, torch.bfloat16)
+    want = [E.checkpoint8_restore(q, b, dtype) for dtype in TYPES] + [E.checkpoint8_wgrad(dY, q, b)]
+    for fill in (0x80, 0x7F, 0xFF):
+        qs = torch.empty((t - 1) * ldq + k, dtype=torch.uint8, device="cuda").fill_(fill).view(torch.int8)
+        bs = torch.empty((t - 1) * lds + 3, dtype=torch.uint8, device="cuda").fill_(fill)
+        q2, b2 = qs.as_strided((t, k), (ldq, 1)), bs.as_strided((t, 3), (lds, 1))
+        q2.copy_(q)
+        b2.copy_(b)
+        got = [E.checkpoint8_restore(q2, b2, dtype) for dtype in TYPES] + [E.checkpoint8_wgrad(dY, q2, b2)]
+        assert all(torch.equal(g, w) for g, w in zip(got, want))
+
+
 def test_seed_in_device_memory(E):
     X = _x(4, 10, 100, torch.bfloat16)
     for value in (5, 2**62 + 12345, -3):
