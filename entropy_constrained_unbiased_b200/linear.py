@@ -93,11 +93,14 @@ def checkpoint_linear(x: torch.Tensor, weight: torch.Tensor, bias=None, *, seed)
     independent; an integer, or a CUDA int64 tensor of one entry for graphs).
     weight [n, k] and bias [n] in x's type, or in any under autocast.
 
+    Gradients are of first order, by backward or autograd.grad; torch.func transforms
+    and forward mode are not supported (torch refuses them).
+
     A backward pass may be captured into a graph, as with F.linear: warm up on the
     capturing stream, and keep no eager autograd graph of the same leaves alive."""
     if x.device.type != "cuda" or weight.device != x.device:
         raise E.EcasqError("checkpoint_linear needs x and weight on one CUDA device; there is no CPU path")
-    if weight.dim() != 2 or x.dim() < 1 or x.shape[-1] != weight.shape[1]:
+    if weight.dim() != 2 or 0 in weight.shape or x.dim() < 1 or x.shape[-1] != weight.shape[1]:
         raise E.EcasqError(f"x [..., k] and weight [n, k] do not match: {list(x.shape)}, {list(weight.shape)}")
     if not torch.is_grad_enabled():
         return F.linear(x, weight, bias)  # nothing is kept

@@ -428,6 +428,22 @@ def test_linear_without_gradients_stores_nothing(E):
     assert L.ecasq_launch_count(0) == before + 1
 
 
+def test_linear_refusals(E):
+    """Layers without inputs or outputs are refused in the forward call, not by the backward pass; second derivatives
+    and transforms by torch."""
+    from entropy_constrained_unbiased_b200.linear import checkpoint_linear
+    x, w = _x(1, 4, 8, torch.float32), _x(2, 6, 8, torch.float32).requires_grad_()
+    for a, b in ((x, w[:0]), (x[:, :0], w[:, :0]), (x, w[:, :4]), (x, w[0])):
+        with pytest.raises(E.EcasqError):
+            checkpoint_linear(a, b, seed=1)
+    y = checkpoint_linear(x.requires_grad_(), w, seed=1)
+    (dw,) = torch.autograd.grad(y.square().sum(), w, create_graph=True)
+    with pytest.raises(RuntimeError):
+        torch.autograd.grad(dw.sum(), w)
+    with pytest.raises(RuntimeError):
+        torch.func.grad(lambda m: checkpoint_linear(x.detach(), m, seed=1).sum())(w.detach())
+
+
 def test_linear_under_autocast(E):
     from entropy_constrained_unbiased_b200.linear import checkpoint_linear
     x, w = _x(1, 20, 64, torch.float32).requires_grad_(), _x(2, 10, 64, torch.float32).requires_grad_()
