@@ -121,10 +121,16 @@ __device__ __forceinline__ int ld_shared_cluster(uint32_t addr) {
 __device__ __forceinline__ void mbar_arrive(uint32_t mbar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(mbar) : "memory");
 }
-// On a barrier of either CTA of the cluster. What is handed over lies in this CTA's
-// shared or tensor memory and was ordered before by a proxy or tcgen05 fence, so the
-// arrival needs no release at cluster scope (which took 2000 clocks per stage of the
-// converters, waiting for all earlier stores).
+// On a barrier of either CTA of the cluster, with the instruction's default release, which
+// orders for threads of this CTA. No thread of the other CTA reads what is handed over: it
+// lies in this CTA's shared or tensor memory, and the thread that waits only issues MMAs,
+// of which this CTA's own tensor core reads, or overwrites, this CTA's part. Write and read
+// so meet inside one SM, where the proxy fence (shared memory) or tcgen05.wait::ld and the
+// tcgen05 fence (tensor memory) before the arrival have finished the former. That is the
+// hardware's working, not a promise of the PTX memory model, which knows no order between
+// the CTAs without cluster scope; release and acquire at cluster scope cost a third of the
+// gradient's speed (16384 x 4096 x 4096: 584 instead of 438 us, and 896 through a warp that
+// relays them), and the tests compare every tile's results with 64 bits.
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t mbar) {
   asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(mbar) : "memory");
 }
