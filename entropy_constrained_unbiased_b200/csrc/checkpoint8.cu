@@ -377,8 +377,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGradThreads, 1)
               if (elected) {
 #pragma unroll
                 for (int j = 0; j < kTok / 16; ++j)  // 16 tokens per MMA: 16 rows of 128 bytes
-                  mma_bf16<2>(acc + out.stage * 256, da + j * (2048 >> 4), db + j * (2048 >> 4), idesc_bf16_mn(256, 256),
-                              add || j > 0);
+                  mma_bf16_pair(acc + out.stage * 256, da + j * (2048 >> 4), db + j * (2048 >> 4),
+                                idesc_bf16_mn(256, 256), add || j > 0);
                 mma_commit<2>(y_empty + 8 * y.stage);
               }
               add = true;

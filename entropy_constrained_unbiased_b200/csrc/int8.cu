@@ -203,7 +203,7 @@ __device__ __forceinline__ void put_output(const Product& p, int64_t token, int6
   static_cast<typename Elem<kType>::T*>(p.Y)[token * p.ldy + channel] = Elem<kType>::put(y);
 }
 
-// -- up to 128 tokens: a tile of 128 channels by kTok tokens per cluster, k split over the
+// -- up to 128 tokens: a tile of 128 channels by all of them per cluster, k split over the
 // cluster's CTAs and joined through distributed shared memory (integers: the order
 // does not matter). Bound by the loads into shared memory: 64 tokens by 16384 x 4096
 // weights take 12.5 us from L2 (67 MB, 5.4 TB/s). --
@@ -221,7 +221,7 @@ struct TileCfg {
 template <int kType, int kTok>
 __global__ void __launch_bounds__(192, 2)
     k_int8_tile(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_x, const Product p,
-                int channel_tiles, int split) {
+                int split) {
   using Cfg = TileCfg<kTok>;
   extern __shared__ unsigned char smem_raw[];
   __shared__ uint64_t bars[2 * Cfg::kStages + 1];
@@ -229,10 +229,9 @@ __global__ void __launch_bounds__(192, 2)
   const uint32_t tiles = (smem_addr(smem_raw) + 1023) & ~1023u;
   const uint32_t full = smem_addr(bars), empty = full + 8 * Cfg::kStages, done = empty + 8 * Cfg::kStages;
   const int warp = __shfl_sync(0xffffffffu, warp_id(), 0), lane = lane_id();
-  const int tile = static_cast<int>(blockIdx.x) / split;
+  const int channel0 = static_cast<int>(blockIdx.x) / split * 128;
   const int part = static_cast<int>(blockIdx.x) % split;
-  const int channel0 = (tile % channel_tiles) * 128;
-  const int token0 = (tile / channel_tiles) * kTok;
+  const int tokens = static_cast<int>(p.m);  // at most kTok
   const int per = (p.pieces + split - 1) / split;
   const int first = part * per;
   const int count = min(p.pieces, first + per) - first;  // at least 1 (the host's choice of split)
@@ -274,7 +273,7 @@ __global__ void __launch_bounds__(192, 2)
           mbar_expect_tx(bar, Cfg::kA + Cfg::kB);
           tma_2d(a, &map_w, (first + i) * kPieceK, channel0, bar);
         }
-        tma_2d(a + Cfg::kA, &map_x, (first + i) * kPieceK, token0, bar);
+        tma_2d(a + Cfg::kA, &map_x, (first + i) * kPieceK, 0, bar);
       }
     }
     if (!ok) at.drain(full, kWaitLimit);  // before the memory is given back
@@ -300,7 +299,6 @@ __global__ void __launch_bounds__(192, 2)
     ok = __all_sync(0xffffffffu, mbar_wait_bounded(done, 0, kWaitLimit));
     tcgen05_after_sync();
     const int64_t channel = channel0 + warp * 32 + lane;
-    const int tokens = static_cast<int>(min(static_cast<int64_t>(kTok), p.m - token0));
     const bool live = ok && channel < p.n;
     const float s = live && split == 1 ? p.sb[channel] : 0.0f;
     const float bias = live && split == 1 && p.bias ? p.bias[channel] : 0.0f;
@@ -314,17 +312,17 @@ __global__ void __launch_bounds__(192, 2)
         tmem_ld32(at, v);
       tcgen05_wait_ld();
       if (split == 1) {
-        const float mine = j0 + lane < tokens ? p.sa[token0 + j0 + lane] : 0.0f;
+        const float mine = j0 + lane < tokens ? p.sa[j0 + lane] : 0.0f;
         if (!__any_sync(0xffffffffu, !plain_scale(mine)) && p.pieces < kMostPieces) {
 #pragma unroll
           for (int j = 0; j < kCols; ++j)
             if (live && j0 + j < tokens)
-              put_output<kType, true>(p, token0 + j0 + j, channel, static_cast<int>(v[j]), p.sa[token0 + j0 + j], s, bias);
+              put_output<kType, true>(p, j0 + j, channel, static_cast<int>(v[j]), p.sa[j0 + j], s, bias);
         } else {
 #pragma unroll
           for (int j = 0; j < kCols; ++j)
             if (live && j0 + j < tokens)
-              put_output<kType>(p, token0 + j0 + j, channel, static_cast<int>(v[j]), p.sa[token0 + j0 + j], s, bias);
+              put_output<kType>(p, j0 + j, channel, static_cast<int>(v[j]), p.sa[j0 + j], s, bias);
         }
       } else {
 #pragma unroll
@@ -342,7 +340,6 @@ __global__ void __launch_bounds__(192, 2)
     cluster_sync_all();
     if (warp < 4) {
       const int64_t channel = channel0 + warp * 32 + lane;
-      const int tokens = static_cast<int>(min(static_cast<int64_t>(kTok), p.m - token0));
       if (channel < p.n) {
         const float s = p.sb[channel], bias = p.bias ? p.bias[channel] : 0.0f;
         constexpr int kAtOnce = 8;  // tokens of this CTA's share whose partial sums are in flight
@@ -357,7 +354,7 @@ __global__ void __launch_bounds__(192, 2)
 #pragma unroll
           for (int u = 0; u < kAtOnce; ++u) {
             const int j = j0 + u * split;
-            if (j < tokens) put_output<kType>(p, token0 + j, channel, static_cast<int>(sum[u]), p.sa[token0 + j], s, bias);
+            if (j < tokens) put_output<kType>(p, j, channel, static_cast<int>(sum[u]), p.sa[j], s, bias);
           }
         }
       }
@@ -377,11 +374,10 @@ cudaError_t int8_tile(const CUtensorMap& map_w, const CUtensorMap& map_x, const 
   using Cfg = TileCfg<kTok>;
   const cudaError_t e = cudaFuncSetAttribute(k_int8_tile<kType, kTok>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::kSmem);
   if (e != cudaSuccess) return e;
-  const int channel_tiles = static_cast<int>((p.n + 127) / 128);
-  const dim3 grid(static_cast<unsigned>(channel_tiles * ((p.m + kTok - 1) / kTok) * split));
+  const dim3 grid(static_cast<unsigned>((p.n + 127) / 128 * split));
   note_launch();
   return launch_kernel(k_int8_tile<kType, kTok>, grid, 192, Cfg::kSmem, st, static_cast<unsigned>(split), p.early, map_w,
-                       map_x, p, channel_tiles, split);
+                       map_x, p, split);
 }
 
 // -- many tokens: a pair of CTAs (cta_group::2) per 256 channels by 256 tokens,
@@ -566,18 +562,17 @@ constexpr int kFewTokens = 2;
 constexpr int64_t kFewBytes = 64 << 10;  // shared memory of the tokens
 constexpr int kFewThreads = 256;
 
-// kIn: the tokens' type, or -1 for rows that are quantised already (A, sa).
+// kIn: the tokens' type, or -1 for rows that are quantised already (A, sa). kM tokens.
 template <int kIn, int kType, int kM>
 __global__ void __launch_bounds__(kFewThreads)
     k_int8_few(const void* X, int64_t ldx, bool wide, const int8_t* __restrict__ B, int64_t ldb,
                const Product p, int64_t k) {
-  extern __shared__ int4 tokens[];  // [m][kp / 16]
+  extern __shared__ int4 tokens[];  // [kM][ceil(k / 16)]
   __shared__ uint32_t part[kFewThreads / 32];
   __shared__ float token_scale[kM];
   constexpr int kAhead = 8;  // pieces of 16 bytes in flight per lane
   const int warp = warp_id(), lane = lane_id();
   const int kp = static_cast<int>((k + 15) / 16);
-  const int m = static_cast<int>(p.m);
   const int64_t step = static_cast<int64_t>(gridDim.x) * (kFewThreads / 32);
   int64_t channel = static_cast<int64_t>(blockIdx.x) * (kFewThreads / 32) + warp;
   const int whole = static_cast<int>(k / 16);  // pieces that end inside the row
@@ -601,7 +596,7 @@ __global__ void __launch_bounds__(kFewThreads)
     // the warps share the tokens out: 8 / kM of them to each
     constexpr int kType1 = kIn < 0 ? 0 : kIn, kWarps = kFewThreads / 32 / kM;
     const int j = warp / kWarps, first = warp % kWarps * 32 + lane;
-    const T* row = x + (j < m ? j : 0) * ldx;
+    const T* row = x + j * ldx;
     Largest<kType1> top;
 #pragma unroll 4
     for (int64_t c = first; c < 2 * kp; c += kWarps * 32) top.add(load8<kType1>(row, c * 8, k, wide));
@@ -609,28 +604,26 @@ __global__ void __launch_bounds__(kFewThreads)
     if (lane == 0) part[warp] = mine;
     __syncthreads();
     const RowScale a = row_scale(__reduce_max_sync(0xffffffffu, part[j * kWarps + lane % kWarps]));
-    if (j < m) {
-      if (first == 0) token_scale[j] = a.scale;
+    if (first == 0) token_scale[j] = a.scale;
 #pragma unroll 4
-      for (int64_t c = first; c < 2 * kp; c += kWarps * 32) {
-        float v[8];
-        floats8<kType1>(load8<kType1>(row, c * 8, k, wide), v);
-        reinterpret_cast<uint2*>(tokens)[static_cast<int64_t>(j) * kp * 2 + c] = quantize8(v, a);
-      }
+    for (int64_t c = first; c < 2 * kp; c += kWarps * 32) {
+      float v[8];
+      floats8<kType1>(load8<kType1>(row, c * 8, k, wide), v);
+      reinterpret_cast<uint2*>(tokens)[static_cast<int64_t>(j) * kp * 2 + c] = quantize8(v, a);
     }
   } else {
     after_previous();
     const int8_t* x = static_cast<const int8_t*>(X);
 #pragma unroll 8
-    for (int i = threadIdx.x; i < m * kp; i += kFewThreads) {
+    for (int i = threadIdx.x; i < kM * kp; i += kFewThreads) {
       const int j = i / kp, c = i - j * kp;
       if (c < whole) tokens[i] = reinterpret_cast<const int4*>(x + j * ldx)[c];
     }
-    for (int i = threadIdx.x; i < m * tail; i += kFewThreads) {
+    for (int i = threadIdx.x; i < kM * tail; i += kFewThreads) {
       const int j = i / tail, c = whole * 16 + i - j * tail;
       reinterpret_cast<int8_t*>(tokens)[static_cast<int64_t>(j) * kp * 16 + c] = x[j * ldx + c];
     }
-    if (threadIdx.x < m) token_scale[threadIdx.x] = p.sa[threadIdx.x];
+    if (threadIdx.x < kM) token_scale[threadIdx.x] = p.sa[threadIdx.x];
   }
   __syncthreads();
 
@@ -639,7 +632,7 @@ __global__ void __launch_bounds__(kFewThreads)
     if (lane < tail) {
 #pragma unroll
       for (int j = 0; j < kM; ++j)
-        if (j < m) acc[j] = last * reinterpret_cast<const int8_t*>(tokens)[(j * kp + whole) * 16 + lane];
+        acc[j] = last * reinterpret_cast<const int8_t*>(tokens)[(j * kp + whole) * 16 + lane];
     }
     for (int at = 0; at < whole; at += 32 * kAhead) {
       if (at > 0) load(channel, at);
@@ -649,7 +642,6 @@ __global__ void __launch_bounds__(kFewThreads)
         if (piece < whole) {
 #pragma unroll
           for (int j = 0; j < kM; ++j) {
-            if (j >= m) break;
             const int4 x = tokens[j * kp + piece];
             acc[j] = __dp4a(w[i].w, x.w, __dp4a(w[i].z, x.z, __dp4a(w[i].y, x.y, __dp4a(w[i].x, x.x, acc[j]))));
           }
@@ -664,7 +656,7 @@ __global__ void __launch_bounds__(kFewThreads)
       const int sum = __reduce_add_sync(0xffffffffu, acc[j]);
       if (lane == j) mine = sum;
     }
-    if (lane < m) put_output<kType>(p, lane, channel, mine, token_scale[lane], s, bias);
+    if (lane < kM) put_output<kType>(p, lane, channel, mine, token_scale[lane], s, bias);
   }
 }
 
@@ -706,8 +698,7 @@ cudaError_t int8_split(const int8_t* A, int64_t lda, const int8_t* B, int64_t ld
                        cudaStream_t st) {
   CUtensorMap map_w, map_x;
   if (!map_rows8(&map_w, B, p.n, k, ldb, 128) || !map_rows8(&map_x, A, p.m, k, lda, kTok)) return cudaErrorInvalidValue;
-  const int64_t tiles = (p.n + 127) / 128 * ((p.m + kTok - 1) / kTok);
-  if (tiles > INT32_MAX / 16) return cudaErrorInvalidValue;
+  const int64_t tiles = (p.n + 127) / 128;
   // Split k while the CTAs leave SMs idle, with at least two pieces each. us with 1 / 2 / 4
   // / 8 parts: 16 tokens by 4096 x 4096 8.4 / 7.2 / 6.4 / 8.0, 128 by 4096 x 4096 17.3 / 16.8
   // / 13.8 / 15.1; 64 by 16384 x 4096 12.5 / 13.9 (a second CTA per SM shares its loads).

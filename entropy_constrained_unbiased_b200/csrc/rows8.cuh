@@ -19,21 +19,18 @@ template <>
 struct Elem<kF32> {
   using T = float;
   using Bits = uint32_t;
-  __device__ __forceinline__ static float get(T v) { return v; }
   __device__ __forceinline__ static T put(float v) { return v; }
 };
 template <>
 struct Elem<kBF16> {
   using T = __nv_bfloat16;
   using Bits = uint16_t;
-  __device__ __forceinline__ static float get(T v) { return __bfloat162float(v); }
   __device__ __forceinline__ static T put(float v) { return __float2bfloat16_rn(v); }
 };
 template <>
 struct Elem<kF16> {
   using T = __half;
   using Bits = uint16_t;
-  __device__ __forceinline__ static float get(T v) { return __half2float(v); }
   __device__ __forceinline__ static T put(float v) { return __float2half_rn(v); }
 };
 

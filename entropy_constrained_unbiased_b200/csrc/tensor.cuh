@@ -188,13 +188,6 @@ __device__ __forceinline__ void tma_2d(uint32_t dst, const CUtensorMap* map, int
       "l"(map), "r"(x), "r"(y), "r"(mbar)
       : "memory");
 }
-__device__ __forceinline__ void tma_3d(uint32_t dst, const CUtensorMap* map, int x, int y, int z, uint32_t mbar) {
-  asm volatile(
-      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], "
-      "[%5];" ::"r"(dst),
-      "l"(map), "r"(x), "r"(y), "r"(z), "r"(mbar)
-      : "memory");
-}
 // The same into this CTA's memory, counted on a barrier of either CTA of the pair
 // (a shared::cluster address, see map_shared).
 __device__ __forceinline__ void tma_2d_pair(uint32_t dst, const CUtensorMap* map, int x, int y, uint32_t mbar) {
@@ -265,12 +258,8 @@ __device__ __forceinline__ void mma_i8(uint32_t d, uint64_t a, uint64_t b, uint3
   else
     ECASQ_MMA("i8", "2");
 }
-template <int kGroup>
-__device__ __forceinline__ void mma_bf16(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add) {
-  if constexpr (kGroup == 1)
-    ECASQ_MMA("f16", "1");
-  else
-    ECASQ_MMA("f16", "2");
+__device__ __forceinline__ void mma_bf16_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add) {
+  ECASQ_MMA("f16", "2");
 }
 #undef ECASQ_MMA
 
