@@ -181,9 +181,10 @@ void piece_grid(int64_t t, int64_t pieces, dim3* grid, dim3* block) {
 // adjacent entries of a row of dW. A pair of CTAs (cta_group::2) takes 256 features
 // by 256 outputs; each CTA converts its own 128 features only.
 //
-// Bound by the tensor cores and their clock (16384 tokens, 4096 x 4096, bfloat16: 420 us,
-// 1.31 PFLOP/s; the 256 tiles are 3.46 rounds of 74 pairs).
-// float32 dY, 4096 tokens, 4096 x 1024: 70 us behind 30 us for its terms.
+// Bound by the tensor cores and their clock, with instruction issue close behind (16384
+// tokens, 4096 x 4096, bfloat16: 420 to 450 us by the clock that the power limit leaves, 1.22
+// to 1.31 PFLOP/s; in 449 us at 1.57 GHz tensor pipe 64%, issue 72%; the 256 tiles are 3.46
+// rounds of 74 pairs). float32 dY, 4096 tokens, 4096 x 1024: 70 us behind 30 us for its terms.
 //
 // The tensor core adds to its float32 accumulator by cutting, not rounding: a step of
 // 16 tokens loses up to 2^-23 of the running sum, always towards zero (measured: 2.2e-6
@@ -544,8 +545,8 @@ __global__ void __launch_bounds__(256)
 }
 
 // How a gradient is cut: the token axis into as many parts as leave pairs idle otherwise, of
-// at least 4 pieces (512 x 512, us in one part and split: 65536 tokens 322 and 39, 4096
-// tokens 31 and 18, where parts of at least 8 pieces took 20; 1024 tokens 16 and 16);
+// at least 4 pieces (512 x 512, us in one part and split: 65536 tokens 350 and 41, 4096
+// tokens 32 and 17.2, where parts of at least 8 pieces took 18.6; 1024 tokens 15.5 and 15.0);
 // bf16 terms and whether dY is copied into them; the workspace.
 struct GradientPlan {
   int terms, split, per;

@@ -20,7 +20,9 @@ namespace {
 // keep it in registers between the two (kKeep pieces of 8 entries each, as they lie in
 // memory), so X is read once; longer rows read the rest again, from L2. Between memory
 // and instruction issue: 3 bytes for a bfloat16 entry leave 16 instructions for it at
-// full bandwidth, and it takes 14 (16384 x 16384 bfloat16: 168 us, 4.8 TB/s, issue 64%).
+// full bandwidth, and it takes 14 (16384 x 16384 bfloat16 activations with outliers: 170
+// us, 4.7 TB/s, issue 64%). Entries that are exactly half the largest are ties, which the
+// fp64 quotient decides: plain normal entries, of which one in 600 is, take 266 us.
 
 // A row's quantisation from its largest magnitude, given as the bits of a float.
 struct RowScale {
@@ -206,7 +208,7 @@ __device__ __forceinline__ void put_output(const Product& p, int64_t token, int6
 // -- up to 128 tokens: a tile of 128 channels by all of them per cluster, k split over the
 // cluster's CTAs and joined through distributed shared memory (integers: the order
 // does not matter). Bound by the loads into shared memory: 64 tokens by 16384 x 4096
-// weights take 12.5 us from L2 (67 MB, 5.4 TB/s). --
+// weights take 11.2 us from L2 (67 MB, 6.0 TB/s). --
 
 template <int kTok>
 struct TileCfg {
@@ -385,7 +387,8 @@ cudaError_t int8_tile(const CUtensorMap& map_w, const CUtensorMap& map_x, const 
 // one is computed. Against the tiles above, with 4096 of k: 128 tokens by 4096 channels
 // 16.6 (tiles: 13.8) us, 256 by 4096 17.0 (19.5), 256 by 16384 18.7 (24.2), 512 by 4096
 // 17.4 (29.3). Bound by the tensor cores: 16384 tokens by 4096 channels by 16384 take
-// 597 us, 3.68 POP/s, with the tensor pipe busy 96% of the time. --
+// 597 to 638 us by the clock that the power limit leaves, 3.4 to 3.7 POP/s, with the tensor
+// pipe busy 96% of the time. --
 
 constexpr int kPairStages = 6;
 constexpr int kPairThreads = 320;  // eight epilogue warps, the producer, the MMA issuer
@@ -680,10 +683,12 @@ cudaError_t int8_few_tokens(const void* X, int64_t ldx, const int8_t* B, int64_t
 }
 
 bool few_tokens(int64_t m, int64_t k) { return m <= kFewTokens && m * ((k + 15) / 16 * 16) <= kFewBytes; }
-// Whether each CTA quantises the tokens itself. That repeats the work in every CTA: one
-// token of 4096 bfloat16 entries takes 7.3 us so and 6.5 us as two launches, but a second
-// launch costs the host 2 us more than that; at 8192 entries it is 11.0 against 8.7, at
-// two tokens of 4096 10.0 against 7.2.
+// Whether each CTA quantises the tokens itself. That repeats the work in every CTA, but
+// spares a caller the second launch and its workspace. bfloat16, 4096 channels, us in a
+// graph and from Python, so / as two launches: one token of 1024 entries 5.0 / 5.2 and 11.2
+// / 15.6, of 2048 5.3 / 5.1, of 4096 7.5 / 6.4 and 11.1 / 15.5, of 8192 10.6 / 8.5 and 12.3 /
+// 15.6, two of 2048 6.4 / 5.6, two of 4096 9.4 / 7.3; 16384 channels, one of 4096 12.2 / 10.0
+// and 14.4 / 15.5. So up to 4096 entries, where a graph loses no more than a launch gains.
 bool few_entries(int64_t m, int64_t k) { return few_tokens(m, k) && m * k <= 4096; }
 
 // A map of 8-bit rows in boxes of 128 bytes by `rows`.
